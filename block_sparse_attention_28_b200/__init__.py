@@ -29,6 +29,9 @@ STA_ERR_CUDA = 4
 STA_ERR_TIMEOUT = 5
 STA_ERR_BAD_MASK = 6
 STA_ERR_BOUNDS = 7
+STA_ERR_BAD_CACHE = 8
+STA_BF16, STA_FP16 = 0, 1
+PAGE = 64
 MAX_GROUPS = 8
 
 
@@ -54,6 +57,24 @@ class MaskParams(ctypes.Structure):
         ("head_topk_floor", ctypes.c_int32),
         ("block_scores", ctypes.c_void_p),
         ("query_pairs", ctypes.c_void_p),
+    ]
+
+
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("k_pages", ctypes.c_void_p),
+        ("v_pages", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p),
+        ("seen", ctypes.c_void_p),
+        ("slot_pos", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p),
     ]
 
 
@@ -103,6 +124,17 @@ _lib.sta_attn_fwd_block_mass.restype = ctypes.c_int
 _lib.sta_search_windows.argtypes = [_vp, _i32, _i32, Grid, _i32, ctypes.POINTER(ctypes.c_int32), _f32, _f32,
                                     _vp, _vp, _vp]
 _lib.sta_search_windows.restype = ctypes.c_int
+_lib.sta_cache_append.argtypes = [ctypes.POINTER(KvCacheDesc), _vp, _vp, _i32, _vp, _vp]
+_lib.sta_cache_append.restype = ctypes.c_int
+_lib.sta_attn_fwd_cached_workspace.argtypes = [ctypes.POINTER(KvCacheDesc), _i32, _i32, _i32]
+_lib.sta_attn_fwd_cached_workspace.restype = _sz
+_lib.sta_attn_fwd_cached.argtypes = [ctypes.POINTER(KvCacheDesc), _vp, _vp, _vp, _i32, _i32, _vp, _vp, _i64, _i32,
+                                     _vp, _sz, _f32, _vp]
+_lib.sta_attn_fwd_cached.restype = ctypes.c_int
+_lib.sta_cache_evict_workspace.argtypes = [ctypes.POINTER(KvCacheDesc), _i32]
+_lib.sta_cache_evict_workspace.restype = _sz
+_lib.sta_cache_evict.argtypes = [ctypes.POINTER(KvCacheDesc), _i32, _i32, _i32, _vp, _sz, _vp]
+_lib.sta_cache_evict.restype = ctypes.c_int
 _lib.sta_set_wait_limit.argtypes = [_i64]
 _lib.sta_set_wait_limit.restype = ctypes.c_int
 _lib.sta_get_wait_limit.argtypes = []
@@ -303,6 +335,114 @@ def sta_search_windows(block_mass, B, heads, g, group_lo, tau, lam, windows, sta
     _check(_lib.sta_search_windows(_ptr(block_mass), B, heads, g, len(group_lo), lo, float(tau), float(lam),
                                    _ptr(windows), _ptr(stats), _stream(stream)),
            "sta_search_windows")
+
+
+# ------------------------------------------------------------ key-value cache
+class KVCache:
+    """A paged key-value cache over the caller's tensors (include/sta.h,
+    sta_kv_cache): made once, it may be used as long as the tensors live (it
+    keeps them alive). The tensors are checked here, on every call only what
+    that call adds."""
+
+    def __init__(self, k_pages, v_pages, page_table, lens, seen=None, slot_pos=None, weight=None):
+        dtypes = {torch.bfloat16: STA_BF16, torch.float16: STA_FP16}
+        if k_pages.dim() != 4 or k_pages.shape[2] != PAGE or k_pages.dtype not in dtypes:
+            raise ValueError(f"k_pages: bf16 or fp16 [num_pages, kv_heads, {PAGE}, d], "
+                             f"not {k_pages.dtype} {list(k_pages.shape)}")
+        if page_table.dim() != 2 or lens.dim() != 2:
+            raise ValueError("page_table is [B, max_pages], lens is [B, kv_heads]")
+        self.num_pages, self.kv_heads, _, self.d = k_pages.shape
+        self.B, self.max_pages = page_table.shape
+        self.dtype, self.device = k_pages.dtype, k_pages.device
+        rows, slots = (self.B, self.kv_heads), PAGE * self.max_pages
+        self._tensor("k_pages", k_pages, k_pages.dtype, tuple(k_pages.shape))
+        self._tensor("v_pages", v_pages, k_pages.dtype, tuple(k_pages.shape))
+        self._tensor("page_table", page_table, torch.int32, (self.B, self.max_pages))
+        self._tensor("lens", lens, torch.int32, rows)
+        self._tensor("seen", seen, torch.int32, rows, optional=True)
+        self._tensor("slot_pos", slot_pos, torch.int32, rows + (slots,), optional=True)
+        self._tensor("weight", weight, torch.float32, rows + (slots,), optional=True)
+        self.k_pages, self.v_pages, self.page_table, self.lens = k_pages, v_pages, page_table, lens
+        self.seen, self.slot_pos, self.weight = seen, slot_pos, weight
+        self.desc = KvCacheDesc(self.B, self.kv_heads, self.d, dtypes[k_pages.dtype], self.num_pages, self.max_pages,
+                                _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(lens), _ptr(seen),
+                                _ptr(slot_pos), _ptr(weight))
+
+    def _tensor(self, name, t, dtype, shape, optional=False):
+        """A contiguous tensor of this type and shape on the cache's device."""
+        if t is None and optional:
+            return
+        if t is None or t.dtype != dtype or t.device != self.device or not t.is_contiguous() or \
+                (shape is not None and tuple(t.shape) != shape):
+            got = "None" if t is None else f"{t.dtype} {list(t.shape)} strides {list(t.stride())} on {t.device}"
+            raise ValueError(f"{name}: contiguous {dtype} {'' if shape is None else list(shape)} on {self.device}, "
+                             f"not {got}")
+
+    def _call(self, stream, fn, what):
+        """fn(stream) with the cache's device current; torch's current stream
+        of that device unless one is given."""
+        if self.device.type != "cuda":
+            raise ValueError(f"{what}: the cache is on {self.device}, not on a GPU")
+        if self.device.index == torch.cuda.current_device():
+            _check(fn(_stream(stream)), what)
+        else:
+            with torch.cuda.device(self.device):
+                _check(fn(_stream(stream)), what)
+
+
+def kv_cache(k_pages, v_pages, page_table, lens, seen=None, slot_pos=None, weight=None):
+    """KVCache of these tensors."""
+    return KVCache(k_pages, v_pages, page_table, lens, seen, slot_pos, weight)
+
+
+def sta_cache_append(cache, k_new, v_new, counts=None, stream=None):
+    """Writes k_new, v_new [B, n_new, kv_heads, d] behind the cache's tokens;
+    lens (and seen) already count them; counts (int32 [B]): the rows of a
+    padded batch that are tokens."""
+    n_new = k_new.shape[1] if k_new.dim() == 4 else 0
+    shape = (cache.B, n_new, cache.kv_heads, cache.d)
+    cache._tensor("k_new", k_new, cache.dtype, shape)
+    cache._tensor("v_new", v_new, cache.dtype, shape)
+    cache._tensor("counts", counts, torch.int32, (cache.B,), optional=True)
+    cache._call(stream, lambda s: _lib.sta_cache_append(ctypes.byref(cache.desc), _ptr(k_new), _ptr(v_new), n_new,
+                                                        _ptr(counts), s), "sta_cache_append")
+
+
+def sta_attn_fwd_cached_workspace(cache, q_heads, n_q=1, accumulate=False):
+    return int(_lib.sta_attn_fwd_cached_workspace(ctypes.byref(cache.desc), q_heads, n_q, 1 if accumulate else 0))
+
+
+def sta_attn_fwd_cached(cache, q, o, lse, workspace, page_ptr=None, page_idx=None, accumulate=False, sm_scale=0.0,
+                        stream=None):
+    """Attention of the newest tokens q [B, n_q, q_heads, d] over the cache, or
+    over the listed pages of each key head (CSR page_ptr int32
+    [B*kv_heads + 1], page_idx int32); accumulate adds each slot's attention
+    to cache.weight. workspace: uint8, sta_attn_fwd_cached_workspace() bytes."""
+    n_q, q_heads = (q.shape[1], q.shape[2]) if q.dim() == 4 else (0, 0)
+    cache._tensor("q", q, cache.dtype, (cache.B, n_q, q_heads, cache.d))
+    cache._tensor("o", o, cache.dtype, (cache.B, n_q, q_heads, cache.d))
+    cache._tensor("lse", lse, torch.float32, (cache.B, q_heads, n_q), optional=True)
+    cache._tensor("workspace", workspace, torch.uint8, None)
+    cache._tensor("page_ptr", page_ptr, torch.int32, (cache.B * cache.kv_heads + 1,), optional=True)
+    cache._tensor("page_idx", page_idx, torch.int32, None, optional=True)
+    capacity = 0 if page_idx is None else page_idx.numel()
+    # torch has no address for a tensor of no elements: no list is longer than zero
+    idx = _ptr(page_idx if page_idx is None or capacity else page_ptr)
+    cache._call(stream, lambda s: _lib.sta_attn_fwd_cached(
+        ctypes.byref(cache.desc), _ptr(q), _ptr(o), _ptr(lse), q_heads, n_q, _ptr(page_ptr), idx, capacity,
+        1 if accumulate else 0, _ptr(workspace), workspace.numel(), float(sm_scale), s), "sta_attn_fwd_cached")
+
+
+def sta_cache_evict_workspace(cache, budget):
+    return int(_lib.sta_cache_evict_workspace(ctypes.byref(cache.desc), int(budget)))
+
+
+def sta_cache_evict(cache, budget, recent, sinks, workspace, stream=None):
+    """Cuts every (sequence, head) to `budget` slots: the first `sinks` and the
+    `recent` newest positions stay, and the heaviest of the others."""
+    cache._tensor("workspace", workspace, torch.uint8, None)
+    cache._call(stream, lambda s: _lib.sta_cache_evict(ctypes.byref(cache.desc), int(budget), int(recent), int(sinks),
+                                                       _ptr(workspace), workspace.numel(), s), "sta_cache_evict")
 
 
 def sta_set_wait_limit(limit_cycles):

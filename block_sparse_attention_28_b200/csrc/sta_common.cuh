@@ -15,6 +15,7 @@ enum : unsigned int {
   DEV_ERR_TIMEOUT = 1u,
   DEV_ERR_BAD_MASK = 2u,
   DEV_ERR_BOUNDS = 4u,  // checked build only: an index or address failed its check
+  DEV_ERR_BAD_CACHE = 8u,
 };
 
 __device__ unsigned int g_dev_error;

@@ -7,7 +7,9 @@
 #include <mutex>
 
 #include "sta_attn.cuh"
+#include "sta_cache.cuh"
 #include "sta_common.cuh"
+#include "sta_decode.cuh"
 #include "sta_host.cuh"
 #include "sta_mask.cuh"
 #include "sta_pair.cuh"
@@ -416,6 +418,98 @@ sta_status launch_attn(const void *q, const void *k, const void *v, void *o, flo
   return STA_OK;
 }
 
+// Sizes of a cache that every call on it checks.
+sta_status cache_sizes(const sta_kv_cache *c) {
+  if (c == nullptr || c->B < 1 || c->kv_heads < 1 || c->num_pages < 1 || c->max_pages < 1) return STA_ERR_INVALID_ARG;
+  if ((c->d != 64 && c->d != 128) || (c->dtype != STA_BF16 && c->dtype != STA_FP16)) return STA_ERR_UNSUPPORTED;
+  const long long rows = (long long)c->B * c->kv_heads;
+  // rows and rows * max_pages index in 32 bits, the pools' rows are TMA
+  // coordinates, sequences go into grid.y
+  if (c->B > 65535 || rows >= (1LL << 31) || (long long)c->num_pages * c->kv_heads >= (1LL << 31) / cache::PAGE ||
+      c->max_pages > (1 << 30) / cache::PAGE || rows * c->max_pages >= (1LL << 31))
+    return STA_ERR_UNSUPPORTED;
+  return STA_OK;
+}
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+sta_status cache_args(const sta_kv_cache *c, cache::Args *a) {
+  const sta_status st = cache_sizes(c);
+  if (st != STA_OK) return st;
+  if (c->k_pages == nullptr || c->v_pages == nullptr || c->page_table == nullptr || c->lens == nullptr ||
+      !aligned16(c->k_pages) || !aligned16(c->v_pages) || !aligned4(c->page_table) || !aligned4(c->lens) ||
+      !aligned4(c->seen) || !aligned4(c->slot_pos) || !aligned4(c->weight) ||
+      (c->slot_pos != nullptr && c->seen == nullptr))
+    return STA_ERR_INVALID_ARG;
+  a->k = static_cast<uint4 *>(c->k_pages);
+  a->v = static_cast<uint4 *>(c->v_pages);
+  a->table = c->page_table;
+  a->lens = c->lens;
+  a->seen = c->seen;
+  a->pos = c->slot_pos;
+  a->weight = c->weight;
+  a->B = c->B;
+  a->H = c->kv_heads;
+  a->num_pages = c->num_pages;
+  a->max_pages = c->max_pages;
+  return STA_OK;
+}
+
+sta_status decode_sizes(const sta_kv_cache *c, int32_t q_heads, int32_t n_q, int *group) {
+  if (q_heads < 1 || n_q < 1 || q_heads % c->kv_heads != 0) return STA_ERR_INVALID_ARG;
+  *group = q_heads / c->kv_heads;
+  if ((long long)*group * n_q > 64) return STA_ERR_UNSUPPORTED;
+  return STA_OK;
+}
+
+struct DecodeWs {
+  size_t lse, total;
+};
+
+DecodeWs decode_ws_layout(const sta_kv_cache *c, int group, int n_q, bool accumulate) {
+  DecodeWs w;
+  w.lse = 0;
+  w.total = align_up((size_t)c->B * c->kv_heads * group * n_q * sizeof(float), 256);
+  return w;
+}
+
+template <int D, typename T>
+sta_status launch_decode(const sta_kv_cache *c, const cache::Args &a, const decode::Shape &shape, const void *q,
+                         void *o, float *lse, bool accumulate, uint8_t *ws, cudaStream_t s) {
+  const int M = shape.group * shape.n_q;
+  float *lse_rows = reinterpret_cast<float *>(ws);
+  const unsigned rows = (unsigned)(c->B * c->kv_heads);
+  decode::attend_kernel<D, T><<<dim3(rows, M), decode::THREADS, 0, s>>>(
+      a, shape, static_cast<const T *>(q), static_cast<T *>(o), lse, lse_rows);
+  STA_CUDA_TRY(cudaGetLastError());
+  if (accumulate) {
+    const unsigned pages = (unsigned)(c->max_pages < 1024 ? c->max_pages : 1024);
+    decode::weigh_kernel<D, T><<<dim3(rows, pages), cache::PAGE, 0, s>>>(a, shape, static_cast<const T *>(q),
+                                                                         lse_rows);
+    STA_CUDA_TRY(cudaGetLastError());
+  }
+  return STA_OK;
+}
+
+// holes and fills [rows][cap], count [rows]; cap: pairs a row can have
+struct EvictWs {
+  int cap;
+  size_t holes, fills, count, total;
+};
+
+EvictWs evict_ws_layout(const sta_kv_cache *c, int32_t budget) {
+  EvictWs w;
+  const long long slots = (long long)cache::PAGE * c->max_pages;
+  const long long past = slots > budget ? slots - budget : 0;
+  w.cap = (int)(past < budget ? past : budget);
+  const size_t rows = (size_t)c->B * c->kv_heads;
+  w.holes = 0;
+  w.fills = align_up(rows * w.cap * sizeof(int), 256);
+  w.count = w.fills + align_up(rows * w.cap * sizeof(int), 256);
+  w.total = w.count + align_up(rows * sizeof(int), 256);
+  return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -673,6 +767,108 @@ sta_status sta_search_windows(const float *block_mass, int32_t B, int32_t heads,
   return STA_OK;
 }
 
+sta_status sta_cache_append(const sta_kv_cache *cache, const void *k_new, const void *v_new, int32_t n_new,
+                            const int32_t *counts, sta_stream_t stream) {
+  cache::Args a;
+  const sta_status st = cache_args(cache, &a);
+  if (st != STA_OK) return st;
+  if (k_new == nullptr || v_new == nullptr || !aligned16(k_new) || !aligned16(v_new) || !aligned4(counts) ||
+      n_new < 1)
+    return STA_ERR_INVALID_ARG;
+  if ((long long)n_new * cache->kv_heads * cache->d >= (1LL << 31)) return STA_ERR_UNSUPPORTED;
+  if (!device_is_sm100()) return STA_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const long long chunks = (long long)n_new * cache->kv_heads * (cache->d / 8);
+  const long long per_cta = cache::APPEND_THREADS * cache::APPEND_UNROLL;
+  const dim3 grid((unsigned)((chunks + per_cta - 1) / per_cta), (unsigned)cache->B);
+  const uint4 *kn = static_cast<const uint4 *>(k_new), *vn = static_cast<const uint4 *>(v_new);
+  if (cache->d == 128)
+    cache::append_kernel<128><<<grid, cache::APPEND_THREADS, 0, s>>>(a, kn, vn, n_new, counts);
+  else
+    cache::append_kernel<64><<<grid, cache::APPEND_THREADS, 0, s>>>(a, kn, vn, n_new, counts);
+  STA_CUDA_TRY(cudaGetLastError());
+  return STA_OK;
+}
+
+size_t sta_attn_fwd_cached_workspace(const sta_kv_cache *cache, int32_t q_heads, int32_t n_q, int32_t accumulate) {
+  int group;
+  if (cache_sizes(cache) != STA_OK || decode_sizes(cache, q_heads, n_q, &group) != STA_OK) return 0;
+  return decode_ws_layout(cache, group, n_q, accumulate != 0).total;
+}
+
+sta_status sta_attn_fwd_cached(const sta_kv_cache *cache, const void *q, void *o, float *lse, int32_t q_heads,
+                               int32_t n_q, const int32_t *page_ptr, const int32_t *page_idx,
+                               int64_t idx_capacity, int32_t accumulate, void *workspace, size_t ws_bytes,
+                               float sm_scale, sta_stream_t stream) {
+  cache::Args a;
+  int group = 0;
+  sta_status st = cache_args(cache, &a);
+  if (st == STA_OK) st = decode_sizes(cache, q_heads, n_q, &group);
+  if (st != STA_OK) return st;
+  if (q == nullptr || o == nullptr || !aligned16(q) || !aligned16(o) || !aligned4(lse) || !aligned4(page_ptr) ||
+      !aligned4(page_idx))
+    return STA_ERR_INVALID_ARG;
+  if ((page_ptr == nullptr) != (page_idx == nullptr) || idx_capacity < 0 ||
+      (page_ptr == nullptr && idx_capacity != 0))
+    return STA_ERR_INVALID_ARG;
+  if (accumulate != 0 && (accumulate != 1 || a.weight == nullptr)) return STA_ERR_INVALID_ARG;
+  if (!(sm_scale == sm_scale) || sm_scale < 0.0f) return STA_ERR_INVALID_ARG;
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      ws_bytes < decode_ws_layout(cache, group, n_q, accumulate != 0).total)
+    return STA_ERR_WORKSPACE;
+  if (!device_is_sm100()) return STA_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  decode::Shape shape;
+  shape.group = group;
+  shape.n_q = n_q;
+  shape.page_ptr = page_ptr;
+  shape.page_idx = page_idx;
+  shape.idx_capacity = idx_capacity;
+  shape.scale = sm_scale != 0.0f ? sm_scale : 1.0f / sqrtf((float)cache->d);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  if (cache->dtype == STA_FP16)
+    return cache->d == 128 ? launch_decode<128, __half>(cache, a, shape, q, o, lse, accumulate != 0, ws, s)
+                           : launch_decode<64, __half>(cache, a, shape, q, o, lse, accumulate != 0, ws, s);
+  return cache->d == 128 ? launch_decode<128, __nv_bfloat16>(cache, a, shape, q, o, lse, accumulate != 0, ws, s)
+                         : launch_decode<64, __nv_bfloat16>(cache, a, shape, q, o, lse, accumulate != 0, ws, s);
+}
+
+size_t sta_cache_evict_workspace(const sta_kv_cache *cache, int32_t budget) {
+  if (cache_sizes(cache) != STA_OK || budget < 1) return 0;
+  return evict_ws_layout(cache, budget).total;
+}
+
+sta_status sta_cache_evict(const sta_kv_cache *cache, int32_t budget, int32_t recent, int32_t sinks,
+                           void *workspace, size_t ws_bytes, sta_stream_t stream) {
+  cache::Args a;
+  const sta_status st = cache_args(cache, &a);
+  if (st != STA_OK) return st;
+  if (a.seen == nullptr || a.pos == nullptr || a.weight == nullptr) return STA_ERR_INVALID_ARG;
+  if (budget < 1 || recent < 0 || sinks < 0 || (long long)recent + sinks > budget) return STA_ERR_INVALID_ARG;
+  const EvictWs w = evict_ws_layout(cache, budget);
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || ws_bytes < w.total)
+    return STA_ERR_WORKSPACE;
+  if (!device_is_sm100()) return STA_ERR_UNSUPPORTED;
+  if (w.cap == 0) return STA_OK;  // the page table holds no more than the budget
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  int *holes = reinterpret_cast<int *>(ws + w.holes), *fills = reinterpret_cast<int *>(ws + w.fills);
+  int *count = reinterpret_cast<int *>(ws + w.count);
+  const unsigned rows = (unsigned)(cache->B * cache->kv_heads);
+  cache::evict_plan_kernel<<<rows, cache::PLAN_THREADS, 0, s>>>(a, budget, recent, sinks, w.cap, holes, fills,
+                                                                count);
+  STA_CUDA_TRY(cudaGetLastError());
+  const int pairs = cache->d == 128 ? cache::move_pairs<128>() : cache::move_pairs<64>();
+  const long long passes = ((long long)w.cap + pairs - 1) / pairs;
+  const dim3 grid(rows, (unsigned)(passes < 65535 ? passes : 65535));
+  if (cache->d == 128)
+    cache::move_kernel<128><<<grid, cache::MOVE_THREADS, 0, s>>>(a, w.cap, holes, fills, count);
+  else
+    cache::move_kernel<64><<<grid, cache::MOVE_THREADS, 0, s>>>(a, w.cap, holes, fills, count);
+  STA_CUDA_TRY(cudaGetLastError());
+  return STA_OK;
+}
+
 sta_status sta_set_wait_limit(int64_t limit_cycles) {
   if (limit_cycles != 0 && (limit_cycles < 1000 || limit_cycles > DEFAULT_WAIT_LIMIT)) return STA_ERR_INVALID_ARG;
   g_wait_limit.store((long long)limit_cycles, std::memory_order_relaxed);
@@ -713,6 +909,7 @@ sta_status sta_get_device_error(sta_stream_t stream) {
   if (word & DEV_ERR_BOUNDS) return STA_ERR_BOUNDS;
   if (word & DEV_ERR_TIMEOUT) return STA_ERR_TIMEOUT;
   if (word & DEV_ERR_BAD_MASK) return STA_ERR_BAD_MASK;
+  if (word & DEV_ERR_BAD_CACHE) return STA_ERR_BAD_CACHE;
   return STA_OK;
 }
 
@@ -728,6 +925,7 @@ const char *sta_status_string(sta_status s) {
     case STA_ERR_TIMEOUT: return "device pipeline wait timed out";
     case STA_ERR_BAD_MASK: return "CSR column index out of range";
     case STA_ERR_BOUNDS: return "index or address outside its buffer (checked build)";
+    case STA_ERR_BAD_CACHE: return "cache length, count or page number out of range";
   }
   return "unknown status";
 }

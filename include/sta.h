@@ -49,9 +49,13 @@ typedef enum {
   STA_ERR_TIMEOUT = 5,     /* device: a bounded pipeline wait ran out */
   STA_ERR_BAD_MASK = 6,    /* device: a CSR column index or query pair out of
                               range, or a CSR that sta_validate_csr rejects */
-  STA_ERR_BOUNDS = 7       /* device, checked build only: an index or address
+  STA_ERR_BOUNDS = 7,      /* device, checked build only: an index or address
                               failed its bounds / alignment check; the access
                               was skipped (see sta_debug_build) */
+  STA_ERR_BAD_CACHE = 8    /* device: a length outside the page table, a count
+                              outside its range, or a page number outside the
+                              pool; what it concerns was left out (see
+                              sta_kv_cache) */
 } sta_status;
 
 typedef struct {
@@ -355,6 +359,112 @@ sta_status sta_search_windows(const float *block_mass, int32_t B, int32_t heads,
                               int32_t num_groups, const int32_t *group_lo, float tau, float lambda,
                               int32_t *windows, float *stats, sta_stream_t stream);
 
+/* sta_kv_cache -- a paged key-value cache of B sequences, for models whose
+ * tokens arrive one after another (or a few, or a prompt at a time). The pages
+ * on video transformers have no counterpart: they attend over a whole clip at
+ * once; a model that generates in order keeps the earlier keys and values and
+ * attends over those. A page is the library's 64-token tile: 64 x d
+ * contiguous elements per head, so block-sparse attention over a cache takes
+ * per-head page lists in the CSR form of the tile lists.
+ *   - Slot j of sequence b lies in page page_table[b][j / 64], row j % 64, of
+ *     every head; heads fill the same slots but may hold different tokens in
+ *     them once sta_cache_evict has chosen per head.
+ *   - lens, seen, slot_pos and weight are per (sequence, head). lens counts
+ *     the filled slots; the entries of page_table past the last filled page
+ *     are never read (they may be -1).
+ *   - Sequences may share pages that no call writes (a common prompt); a page
+ *     that sta_cache_append or sta_cache_evict writes belongs to one sequence.
+ *   - A length outside [0, 64*max_pages] empties its (sequence, head) for the
+ *     call, a page number outside [0, num_pages) leaves its tokens out; both
+ *     are recorded as STA_ERR_BAD_CACHE (sta_get_device_error).
+ * All pointers are device memory of the current device, owned by the caller. */
+#define STA_BF16 0
+#define STA_FP16 1
+typedef struct {
+  int32_t B, kv_heads, d;  /* d in {64, 128} */
+  int32_t dtype;           /* STA_BF16 or STA_FP16: of the pages, and of every
+                              q, o, k_new, v_new given with this cache */
+  int32_t num_pages;       /* pages in k_pages and in v_pages;
+                              num_pages * kv_heads * 64 < 2^31 */
+  int32_t max_pages;       /* columns of page_table; B*kv_heads*max_pages < 2^31,
+                              64*max_pages <= 2^30; B <= 65535 */
+  void *k_pages, *v_pages; /* [num_pages, kv_heads, 64, d], 16-byte aligned */
+  const int32_t *page_table; /* [B, max_pages] */
+  int32_t *lens;           /* [B, kv_heads] filled slots */
+  int32_t *seen;           /* [B, kv_heads] tokens the sequence has had, evicted
+                              ones included (= position of its next token), or
+                              NULL when slot_pos is */
+  int32_t *slot_pos;       /* [B, kv_heads, 64*max_pages] position of each slot's
+                              token, or NULL */
+  float *weight;           /* [B, kv_heads, 64*max_pages] attention weight each
+                              slot's token has gathered, or NULL */
+} sta_kv_cache;
+
+/* sta_cache_append -- writes new tokens behind those of a cache.
+ *   k_new, v_new : [B, n_new, kv_heads, d] (raster order)
+ *   counts       : device int32 [B], how many of the n_new rows sequence b has
+ *                  (a padded batch), each in [0, n_new]; NULL: all n_new
+ * The caller counts first: lens (and seen) include the new tokens when the
+ * call runs, so that it changes no length and may be repeated. Row i < counts[b]
+ * goes to slot lens - counts[b] + i, its position seen - counts[b] + i to
+ * slot_pos and 0 to weight, where those arrays are given. Rows from counts[b]
+ * on, and every other slot, are left as they are. A (sequence, head) whose
+ * counts[b] is out of range or exceeds its length is left out, recorded as
+ * STA_ERR_BAD_CACHE. n_new >= 1; n_new * kv_heads * d < 2^31. */
+sta_status sta_cache_append(const sta_kv_cache *cache, const void *k_new, const void *v_new, int32_t n_new,
+                            const int32_t *counts, sta_stream_t stream);
+
+/* sta_attn_fwd_cached -- attention of a sequence's newest tokens over its
+ * cache (block-sparse when page lists are given).
+ *   q, o    : [B, n_q, q_heads, d]; the n_q newest tokens of each sequence,
+ *             already appended; q head j reads key head j / (q_heads / kv_heads)
+ *   lse     : optional fp32 [B, q_heads, n_q] (natural log); NULL to skip
+ *   page_ptr: optional device int32 [B*kv_heads + 1], page_idx int32
+ *             [idx_capacity]: CSR over rows b*kv_heads + h of the page columns
+ *             of page_table a head attends to, ascending and unique; NULL (both,
+ *             idx_capacity 0): every page. An entry that is not above its
+ *             predecessor, or past the last filled page, is skipped and
+ *             recorded as STA_ERR_BAD_MASK, as are offsets that decrease or
+ *             pass idx_capacity
+ *   accumulate : 1: also add to weight[b][h][j] the attention that slot j got,
+ *             sum over the queries i and the q heads of h of e^(s_j - lse);
+ *             slots out of view get nothing added
+ * With s_j = sm_scale q . k_j (sm_scale 0 means 1/sqrt(d)) over the slots j of
+ * the listed pages that query i sees, j < lens - (n_q - 1 - i):
+ *   lse = log(sum_j e^(s_j)),  o = sum_j e^(s_j - lse) v_j.
+ * A query that sees no slot gives o = 0 and lse = -inf. What lies in slots out
+ * of view (infinities and NaN included) has no effect. Sums are fp32; the
+ * weights of the products with V are split in two terms of the cache's type
+ * (a relative error of 2^-16 bf16, 2^-22 fp16).
+ * q_heads is a multiple of kv_heads, n_q * q_heads / kv_heads <= 64.
+ * workspace: device, >= sta_attn_fwd_cached_workspace() bytes (0 for sizes the
+ * call rejects), 256-aligned; nothing in it has to start at zero, and calls
+ * that overlap on the GPU need one each. Deterministic. */
+size_t sta_attn_fwd_cached_workspace(const sta_kv_cache *cache, int32_t q_heads, int32_t n_q, int32_t accumulate);
+sta_status sta_attn_fwd_cached(const sta_kv_cache *cache, const void *q, void *o, float *lse, int32_t q_heads,
+                               int32_t n_q, const int32_t *page_ptr, const int32_t *page_idx,
+                               int64_t idx_capacity, int32_t accumulate, void *workspace, size_t ws_bytes,
+                               float sm_scale, sta_stream_t stream);
+
+/* sta_cache_evict -- cuts every (sequence, head) longer than `budget` slots to
+ * `budget` by accumulated attention weight; shorter ones are left as they are.
+ * The tokens are put in order: first the protected ones, whose position is
+ * below `sinks` or at least seen - recent; then by weight, heaviest first (NaN
+ * below every number); equals by slot. The first `budget` stay. A token that
+ * stays in a slot below `budget` does not move; the i-th that stays in a slot
+ * from `budget` on takes the i-th slot given up below it, with its key, value,
+ * position and weight. lens becomes `budget`; the slots behind are left as they
+ * are, and the pages past ceil(budget / 64) are free once all heads are cut.
+ * Slots are therefore not in order of position afterwards; attention does not
+ * depend on it (the tokens appended since are the last ones).
+ * Needs seen, slot_pos and weight. budget >= 1, recent >= 0, sinks >= 0,
+ * recent + sinks <= budget. workspace: device, >= sta_cache_evict_workspace()
+ * bytes, 256-aligned; nothing in it has to start at zero, and calls that
+ * overlap on the GPU need one each. Deterministic. */
+size_t sta_cache_evict_workspace(const sta_kv_cache *cache, int32_t budget);
+sta_status sta_cache_evict(const sta_kv_cache *cache, int32_t budget, int32_t recent, int32_t sinks,
+                           void *workspace, size_t ws_bytes, sta_stream_t stream);
+
 /* sta_set_wait_limit -- how long a stalled pipeline may wait before it is
  * reported. Every pipeline wait of the kernels launched after this call by
  * this process (the attention forms, the tensor-core scores and the raster
@@ -411,7 +521,8 @@ sta_status sta_validate_csr(const int32_t *row_ptr, const int32_t *col_idx, int6
 /* Reads and clears the device error word of the current device after
  * synchronising `stream`. STA_OK if no device-side fault was recorded;
  * STA_ERR_BOUNDS takes precedence over STA_ERR_TIMEOUT (a skipped access is
- * the cause of the wait that ran out), then STA_ERR_BAD_MASK. */
+ * the cause of the wait that ran out), then STA_ERR_BAD_MASK, then
+ * STA_ERR_BAD_CACHE. */
 sta_status sta_get_device_error(sta_stream_t stream);
 
 /* Static description of a status code. */

@@ -4,12 +4,11 @@
 // bounds them: a key or value row (128 or 256 B) is read once and written once
 // with 16-byte accesses.
 #pragma once
+#include "sta_cache_index.h"
 #include "sta_common.cuh"
 
 namespace sta {
 namespace cache {
-
-constexpr int PAGE = 64;  // tokens a page holds: the library's tile
 
 // sta_kv_cache as the kernels take it.
 struct Args {
@@ -21,7 +20,7 @@ struct Args {
   // length of row r = b*H + h, or -1 (recorded) if the page table cannot hold it
   __device__ __forceinline__ int length(int r) const {
     const int n = lens[r];
-    if (n >= 0 && n <= PAGE * max_pages) return n;
+    if (length_ok(n, max_pages)) return n;
     record_error(DEV_ERR_BAD_CACHE);
     return -1;
   }
@@ -29,7 +28,7 @@ struct Args {
   // 0 <= j < PAGE * max_pages
   __device__ __forceinline__ int page(int b, int j) const {
     const int p = table[(long long)b * max_pages + j / PAGE];
-    if (p >= 0 && p < num_pages) return p;
+    if (page_ok(p, num_pages)) return p;
     record_error(DEV_ERR_BAD_CACHE);
     return -1;
   }

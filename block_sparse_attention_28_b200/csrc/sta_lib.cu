@@ -462,33 +462,83 @@ sta_status decode_sizes(const sta_kv_cache *c, int32_t q_heads, int32_t n_q, int
   return STA_OK;
 }
 
+// Workspace of the attention over a cache: per CTA two parts of rows cut by
+// its chunk's borders and their description; with accumulation also, per page
+// read, its row and column and its scores, and each row's log-sum-exp.
 struct DecodeWs {
-  size_t lse, total;
+  size_t part_o, part_ml, split, units, scores, lse2, total;
 };
 
 DecodeWs decode_ws_layout(const sta_kv_cache *c, int group, int n_q, bool accumulate) {
+  const size_t M = (size_t)group * n_q, parts = 2 * (size_t)decode::MAX_CTAS;
+  const size_t rows = (size_t)c->B * c->kv_heads, units = accumulate ? rows * c->max_pages : 0;
   DecodeWs w;
-  w.lse = 0;
-  w.total = align_up((size_t)c->B * c->kv_heads * group * n_q * sizeof(float), 256);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 256);
+    return at;
+  };
+  w.part_o = take(parts * M * c->d * sizeof(float));
+  w.part_ml = take(parts * M * sizeof(float2));
+  w.split = take(decode::MAX_CTAS * sizeof(decode::Split));
+  w.units = take(units * sizeof(int2));
+  w.scores = take(units * M * cache::PAGE * sizeof(float));
+  w.lse2 = take(accumulate ? rows * M * sizeof(float) : 0);
+  w.total = off;
   return w;
 }
 
-template <int D, typename T>
+template <int D, typename T, bool MASS>
 sta_status launch_decode(const sta_kv_cache *c, const cache::Args &a, const decode::Shape &shape, const void *q,
-                         void *o, float *lse, bool accumulate, uint8_t *ws, cudaStream_t s) {
+                         void *o, float *lse, uint8_t *ws, cudaStream_t s) {
+  using C = decode::Cfg<D>;
   const int M = shape.group * shape.n_q;
-  float *lse_rows = reinterpret_cast<float *>(ws);
-  const unsigned rows = (unsigned)(c->B * c->kv_heads);
-  decode::attend_kernel<D, T><<<dim3(rows, M), decode::THREADS, 0, s>>>(
-      a, shape, static_cast<const T *>(q), static_cast<T *>(o), lse, lse_rows);
+  const DecodeWs w = decode_ws_layout(c, shape.group, shape.n_q, MASS);
+  decode::Work work;
+  work.part_o = reinterpret_cast<float *>(ws + w.part_o);
+  work.part_ml = reinterpret_cast<float2 *>(ws + w.part_ml);
+  work.split = reinterpret_cast<decode::Split *>(ws + w.split);
+  work.units = reinterpret_cast<int2 *>(ws + w.units);
+  work.scores = reinterpret_cast<float *>(ws + w.scores);
+  work.lse2 = reinterpret_cast<float *>(ws + w.lse2);
+  decode::Sink<D, T> sink;
+  sink.o = static_cast<T *>(o);
+  sink.lse = lse;
+  CUtensorMap tk, tv;
+  const unsigned long long pool_rows = (unsigned long long)c->num_pages * c->kv_heads * cache::PAGE;
+  if (!make_tile_map(&tk, c->k_pages, pool_rows, D) || !make_tile_map(&tv, c->v_pages, pool_rows, D))
+    return STA_ERR_CUDA;
+  auto attend = decode::attend_kernel<D, T, MASS>;
+  STA_CUDA_TRY(cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+  const long long most = (long long)c->B * c->kv_heads * c->max_pages;
+  const int sms = sm_count() < decode::MAX_CTAS ? sm_count() : decode::MAX_CTAS;
+  const unsigned ctas = (unsigned)(most < sms ? most : sms);
+  attend<<<ctas, decode::THREADS, C::SMEM, s>>>(tk, tv, a, shape, static_cast<const T *>(q), sink, work, wait_limit());
   STA_CUDA_TRY(cudaGetLastError());
-  if (accumulate) {
-    const unsigned pages = (unsigned)(c->max_pages < 1024 ? c->max_pages : 1024);
-    decode::weigh_kernel<D, T><<<dim3(rows, pages), cache::PAGE, 0, s>>>(a, shape, static_cast<const T *>(q),
-                                                                         lse_rows);
-    STA_CUDA_TRY(cudaGetLastError());
-  }
+  // The join may start up while attend_kernel runs; it waits for its end
+  // before it reads anything.
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, MASS ? decode::JOIN_SHARES : 1);
+  cfg.blockDim = dim3(decode::JOIN_THREADS);
+  cfg.dynamicSmemBytes = (size_t)ctas * M * sizeof(float);
+  cfg.stream = s;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  STA_CUDA_TRY(cudaLaunchKernelEx(&cfg, decode::join_kernel<D, T, MASS>, a, shape,
+                                  static_cast<const decode::Sink<D, T>>(sink),
+                                  static_cast<const decode::Work>(work)));
   return STA_OK;
+}
+
+template <int D, typename T>
+sta_status launch_decode_any(const sta_kv_cache *c, const cache::Args &a, const decode::Shape &shape, const void *q,
+                             void *o, float *lse, bool accumulate, uint8_t *ws, cudaStream_t s) {
+  return accumulate ? launch_decode<D, T, true>(c, a, shape, q, o, lse, ws, s)
+                    : launch_decode<D, T, false>(c, a, shape, q, o, lse, ws, s);
 }
 
 // holes and fills [rows][cap], count [rows]; cap: pairs a row can have
@@ -824,13 +874,14 @@ sta_status sta_attn_fwd_cached(const sta_kv_cache *cache, const void *q, void *o
   shape.page_ptr = page_ptr;
   shape.page_idx = page_idx;
   shape.idx_capacity = idx_capacity;
-  shape.scale = sm_scale != 0.0f ? sm_scale : 1.0f / sqrtf((float)cache->d);
+  shape.scale_log2 = (sm_scale != 0.0f ? sm_scale : 1.0f / sqrtf((float)cache->d)) * 1.4426950408889634f;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
+  const bool acc = accumulate != 0;
   if (cache->dtype == STA_FP16)
-    return cache->d == 128 ? launch_decode<128, __half>(cache, a, shape, q, o, lse, accumulate != 0, ws, s)
-                           : launch_decode<64, __half>(cache, a, shape, q, o, lse, accumulate != 0, ws, s);
-  return cache->d == 128 ? launch_decode<128, __nv_bfloat16>(cache, a, shape, q, o, lse, accumulate != 0, ws, s)
-                         : launch_decode<64, __nv_bfloat16>(cache, a, shape, q, o, lse, accumulate != 0, ws, s);
+    return cache->d == 128 ? launch_decode_any<128, __half>(cache, a, shape, q, o, lse, acc, ws, s)
+                           : launch_decode_any<64, __half>(cache, a, shape, q, o, lse, acc, ws, s);
+  return cache->d == 128 ? launch_decode_any<128, __nv_bfloat16>(cache, a, shape, q, o, lse, acc, ws, s)
+                         : launch_decode_any<64, __nv_bfloat16>(cache, a, shape, q, o, lse, acc, ws, s);
 }
 
 size_t sta_cache_evict_workspace(const sta_kv_cache *cache, int32_t budget) {

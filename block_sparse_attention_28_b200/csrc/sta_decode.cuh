@@ -12,9 +12,10 @@
 // attend_kernel: one CTA per SM. The pages to be read are the units of work,
 // rows one after another, cut into one equal chunk per CTA whatever the
 // lengths are: no CTA waits for a long sequence. A producer warp streams pages
-// through a ring of shared memory (TMA, 128-byte swizzle); 8 warps take pages
-// in turn, each with a running maximum and sum and its own output tile, and are
-// merged where a row ends. Rows cut by a chunk border leave their parts (sum
+// through a ring of shared memory (TMA, 128-byte swizzle). Eight warps take
+// them: two to a page (32 of its slots each), once for every 16 query rows, and
+// with fewer than 64 query rows two or four pages at a time. Each has a running
+// maximum and sum and its own output tile; they are merged where a row ends. Rows cut by a chunk border leave their parts (sum
 // relative to a maximum) in the workspace.
 // join_kernel: joins those parts, and adds every slot's attention to its
 // weight once the row's log-sum-exp is known, from the scores that
@@ -34,6 +35,7 @@ using cache::PAGE;
 
 constexpr int CONSUMERS = 8;  // warps
 constexpr int THREADS = 32 * (CONSUMERS + 1);
+constexpr int KEYS = PAGE / 2;  // slots of a page one warp takes
 constexpr int MAX_ROWS = 64;   // query rows per key head
 constexpr int MAX_CTAS = 148;  // one per SM of a B200
 constexpr int LEAST_UNITS = 1;
@@ -47,6 +49,10 @@ struct Cfg {
   static constexpr int TILE_BYTES = HALF_BYTES * (D / 64);  // keys or values of a page
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
   static constexpr int STAGES = 131072 / STAGE_BYTES;
+  // A warp waits for a stage's next load only after it has had the load before
+  // it, because page groups (4, 2 or 1) divide the stages: a barrier's phase
+  // parity is read one phase ahead at most.
+  static_assert(STAGES % 4 == 0, "page groups divide the stages");
   static constexpr int MERGE_STRIDE = D + 8;  // floats; 8 more spread the rows over the banks
   static constexpr int MERGE_BYTES = CONSUMERS * 16 * MERGE_STRIDE * 4;
   static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + MERGE_BYTES;
@@ -129,10 +135,6 @@ __device__ __forceinline__ void ldmatrix_trans(uint32_t addr, uint32_t (&r)[4]) 
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ void consumer_barrier() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * CONSUMERS) : "memory");
-}
-
 // ------------------------------------------------------------------- rows
 struct RowPages {
   int len, n, first;  // length, pages attended to, first entry of its list
@@ -305,22 +307,22 @@ __device__ __forceinline__ void load_queries(const T *q, const Args &a, const Sh
   }
 }
 
-// One page: scores, softmax step, weighted values. lim[x]: slots of the page
-// that row g + 8 x sees; `held`: slots of the page that are filled. edge: any
-// of them is below PAGE. scores: where this tile's scores go (MASS), M rows in
-// all of which `rows` belong to the tile.
+// KEYS slots of a page (kt, vt: where their keys and values begin): scores, softmax step, weighted
+// values. lim[x]: how many of them row g + 8 x sees; held: how many are filled
+// (either may be negative or above KEYS). edge: any of these is below KEYS.
+// scores: where this tile's scores go (MASS), of which it has `rows` rows.
 template <int D, typename T, bool MASS>
-__device__ __forceinline__ void attend_page(uint32_t kt, uint32_t vt, const uint32_t (&qa)[D / 16][4],
-                                            const Shape &s, int mt, const int (&lim)[2], int held, bool edge,
-                                            Tile<D> &acc, float *scores, int rows) {
+__device__ __forceinline__ void attend_slots(uint32_t kt, uint32_t vt, const uint32_t (&qa)[D / 16][4],
+                                             const Shape &s, const int (&lim)[2], int held, bool edge, Tile<D> &acc,
+                                             float *scores, int rows) {
   using N = Num<T>;
   constexpr int HALF_BYTES = Cfg<D>::HALF_BYTES;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  float p[PAGE / 8][4];
+  float p[KEYS / 8][4];
   {
     const uint32_t row = kt + (lane & 7) * 128, x = lane & 7, m = lane >> 3;
 #pragma unroll
-    for (int n = 0; n < PAGE / 8; ++n) {
+    for (int n = 0; n < KEYS / 8; ++n) {
       p[n][0] = p[n][1] = p[n][2] = p[n][3] = 0.0f;
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
@@ -333,7 +335,7 @@ __device__ __forceinline__ void attend_page(uint32_t kt, uint32_t vt, const uint
     }
   }
 #pragma unroll
-  for (int n = 0; n < PAGE / 8; ++n)
+  for (int n = 0; n < KEYS / 8; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       p[n][e] *= s.scale_log2;
@@ -341,7 +343,7 @@ __device__ __forceinline__ void attend_page(uint32_t kt, uint32_t vt, const uint
     }
   if (MASS) {
 #pragma unroll
-    for (int n = 0; n < PAGE / 8; ++n)
+    for (int n = 0; n < KEYS / 8; ++n)
 #pragma unroll
       for (int x = 0; x < 2; ++x)
         if (g + 8 * x < rows)
@@ -353,7 +355,7 @@ __device__ __forceinline__ void attend_page(uint32_t kt, uint32_t vt, const uint
   for (int x = 0; x < 2; ++x) {
     float up = -INFINITY;
 #pragma unroll
-    for (int n = 0; n < PAGE / 8; ++n) up = tc::fmax3(up, p[n][2 * x], p[n][2 * x + 1]);
+    for (int n = 0; n < KEYS / 8; ++n) up = tc::fmax3(up, p[n][2 * x], p[n][2 * x + 1]);
     up = fmaxf(up, __shfl_xor_sync(0xFFFFFFFFu, up, 1));
     up = fmaxf(up, __shfl_xor_sync(0xFFFFFFFFu, up, 2));
     up = fmaxf(up, acc.top[x]);
@@ -375,7 +377,7 @@ __device__ __forceinline__ void attend_page(uint32_t kt, uint32_t vt, const uint
   for (int x = 0; x < 2; ++x) {
     float z = 0.0f;
 #pragma unroll
-    for (int n = 0; n < PAGE / 8; ++n)
+    for (int n = 0; n < KEYS / 8; ++n)
 #pragma unroll
       for (int e = 2 * x; e < 2 * x + 2; ++e) {
         p[n][e] = tc::ex2(p[n][e] - base[x]);
@@ -413,7 +415,7 @@ __device__ __forceinline__ void attend_page(uint32_t kt, uint32_t vt, const uint
   };
   bool odd = false;
   if (edge && s.n_q > 1) {
-    for (int key = max(0, held - (s.n_q - 1)) + g; key < min(PAGE, held); key += 8)
+    for (int key = max(0, held - (s.n_q - 1)) + g; key < min(KEYS, held); key += 8)
       for (int c = 0; c < D / 8; ++c) {
         const uint32_t v = value_pair(key, c);
         odd |= finite(v) != v;
@@ -421,7 +423,7 @@ __device__ __forceinline__ void attend_page(uint32_t kt, uint32_t vt, const uint
     odd = __any_sync(0xFFFFFFFFu, odd);
   }
 #pragma unroll
-  for (int ks = 0; ks < PAGE / 16; ++ks) {
+  for (int ks = 0; ks < KEYS / 16; ++ks) {
     // the weights of slots 16 ks .. 16 ks + 15 as the A operand, split in two
     // terms: one alone would be off by as much as the output's own rounding
     uint32_t hi[4], lo[4];
@@ -455,7 +457,7 @@ __device__ __forceinline__ void attend_page(uint32_t kt, uint32_t vt, const uint
     }
   }
   if (odd)
-    for (int key = 0; key < min(PAGE, held); ++key)
+    for (int key = 0; key < min(KEYS, held); ++key)
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
         const uint32_t v = value_pair(key, c);
@@ -501,13 +503,13 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
   float *merge = reinterpret_cast<float *>(ring + C::STAGES * C::STAGE_BYTES);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rows = a.B * a.H, M = s.group * s.n_q;
-  // warps side by side over the query rows, the others over the pages
-  const int tiles = M <= 16 ? 1 : (M <= 32 ? 2 : 4), groups = CONSUMERS / tiles;
+  // two warps per page and 16 query rows; the rest side by side over the pages
+  const int tiles = M <= 16 ? 1 : (M <= 32 ? 2 : 4), groups = CONSUMERS / (2 * tiles);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       tc::mbar_init(&full[i], 1);
-      tc::mbar_init(&empty[i], tiles);
+      tc::mbar_init(&empty[i], 2 * tiles);
     }
     abort = 0u;
     tc::fence_barrier_init();
@@ -551,11 +553,13 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
   split.start[0] = split.start[1] = split.n[0] = split.n[1] = 0;
   split.chunk = chunk;
   split.units = units;
-  const int mt = warp % tiles, pg = warp / tiles, g = lane >> 2, t = lane & 3;
+  const int mt = warp % tiles, pg = warp / tiles / 2, g = lane >> 2, t = lane & 3;
+  const int key0 = warp / tiles % 2 * KEYS;
   const int tile_rows = min(16, M - 16 * mt);  // may be <= 0
   int u = u0, row = u0 < u1 ? begin[0] : 0, off = u0 < u1 ? begin[1] : 0;
   int done = 0;  // units of this CTA before the row's
   bool ok = true;
+  bool pending = false;  // a merge that all warps read may still be being read
   Window win;
   if (u0 < u1) win.load(a, s, row, rows);
   Tile<D> acc;
@@ -595,14 +599,14 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
         if (ok) ok = tc::mbar_wait(&full[stage], (it / C::STAGES) & 1, &abort, limit);
         ok = __all_sync(0xFFFFFFFFu, ok);
         const int col = ok ? stage_col[stage] : -1;
-        if (MASS && lane == 0 && mt == 0) work.units[u + x] = make_int2(row, col);
+        if (MASS && lane == 0 && mt == 0 && key0 == 0) work.units[u + x] = make_int2(row, col);
         if (col >= 0 && tile_rows > 0) {
-          const int held = len - col * PAGE;
+          const int held = len - col * PAGE - key0;
           const int lim[2] = {held - back0, held - back1};
-          const uint32_t kt = tc::smem_u32(ring + stage * C::STAGE_BYTES);
-          float *sc = MASS ? work.scores + ((long long)(u + x) * M + 16 * mt) * PAGE : nullptr;
-          attend_page<D, T, MASS>(kt, kt + C::TILE_BYTES, qa, s, mt, lim, held, held - (s.n_q - 1) < PAGE, acc, sc,
-                                  tile_rows);
+          const uint32_t kt = tc::smem_u32(ring + stage * C::STAGE_BYTES) + key0 * 128;
+          float *sc = MASS ? work.scores + ((long long)(u + x) * M + 16 * mt) * PAGE + key0 : nullptr;
+          attend_slots<D, T, MASS>(kt, kt + C::TILE_BYTES, qa, s, lim, held, held - (s.n_q - 1) < KEYS, acc, sc,
+                                   tile_rows);
         }
         __syncwarp();
         if (lane == 0 && ok) tc::mbar_arrive(&empty[stage]);
@@ -630,20 +634,15 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
         if (d == 0) work.part_ml[(long long)part * M + m] = make_float2(top, sum);
       }
     };
-    if (seg == 1) {
-      // one page: the warps that have it hold the result
-      if (active) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (g + 8 * x < tile_rows) {
-            const float top = (acc.top[x] == -INFINITY ? 0.0f : acc.top[x]) - Num<T>::SHIFT;
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-              put(16 * mt + g + 8 * x, 8 * c + 2 * t, acc.o[c][2 * x], acc.o[c][2 * x + 1], top, acc.sum[x]);
-          }
-      }
-    } else {
-      consumer_barrier();  // the last row's merge has been read
+    // The parts go through shared memory: one is written when the merge before
+    // has been read, and read when all are written. All warps take part, or,
+    // where the row has a single page here, that page's.
+    auto everyone = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * CONSUMERS) : "memory"); };
+    auto page_warps = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(2 + pg), "r"(64 * tiles) : "memory"); };
+    if (seg > 1 || pending) everyone();
+    pending = seg > 1;
+    if (seg > 1 || lead == 0) {
+      if (seg == 1) page_warps();
       if (active) {
 #pragma unroll
         for (int x = 0; x < 2; ++x)
@@ -655,17 +654,22 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
             if (t == 0) merge_ml[warp][g + 8 * x] = make_float2(acc.top[x], acc.sum[x]);
           }
       }
-      consumer_barrier();
+      if (seg == 1)
+        page_warps();
+      else
+        everyone();
       const int from = done % groups, have = min(groups, seg);  // page groups that hold a part
-      for (int e = tid; e < M * (D / 2); e += 32 * CONSUMERS) {
+      const int threads = seg == 1 ? 64 * tiles : 32 * CONSUMERS;
+      for (int e = seg == 1 ? tid - pg * 64 * tiles : tid; e < M * (D / 2); e += threads) {
         const int m = e / (D / 2), d = e % (D / 2) * 2;
         const int wt = m >> 4, wr = m & 15;
+        auto holder = [&](int x) { return ((from + (x >> 1)) % groups * 2 + (x & 1)) * tiles + wt; };
         float top = -INFINITY;
-        for (int x = 0; x < have; ++x) top = fmaxf(top, merge_ml[(from + x) % groups * tiles + wt][wr].x);
+        for (int x = 0; x < 2 * have; ++x) top = fmaxf(top, merge_ml[holder(x)][wr].x);
         const float at = top == -INFINITY ? 0.0f : top;
         float sum = 0.0f, o0 = 0.0f, o1 = 0.0f;
-        for (int x = 0; x < have; ++x) {
-          const int w = (from + x) % groups * tiles + wt;
+        for (int x = 0; x < 2 * have; ++x) {
+          const int w = holder(x);
           const float2 ml = merge_ml[w][wr];
           const float f = tc::ex2(ml.x - at);
           const float2 v = *reinterpret_cast<const float2 *>(merge + (w * 16 + wr) * C::MERGE_STRIDE + d);

@@ -275,6 +275,46 @@ def test_a_long_row_and_many_short_ones(sta):
     compare(sta, t, C.queries(41, 1, 4, 64, "bf16", seed=13), "bf16", accumulate=True)
 
 
+@pytest.mark.parametrize("d,dtype,group,n_q", [(128, "bf16", 1, 1), (64, "fp16", 4, 1), (128, "fp16", 9, 2),
+                                               (64, "bf16", 8, 3), (128, "bf16", 7, 9), (64, "fp16", 64, 1)])
+def test_many_pages_to_a_cta(sta, d, dtype, group, n_q):
+    """Rows of thousands of pages (read again and again from a few): the ring
+    of pages goes round many times, for every number of query rows."""
+    n = [300_017, 200_000]
+    t = C.make([640, 640], 1, d, dtype, seed=40)
+    few = t["page_table"][:, :10]
+    g = torch.Generator().manual_seed(41)
+    cols = [few[b].cpu()[torch.randint(0, 10, (5000,), generator=g)] for b in range(2)]
+    t["page_table"] = torch.stack(cols).cuda().contiguous()
+    t["lens"] = torch.tensor(n, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    t["seen"], t["slot_pos"] = None, None
+    t["weight"] = torch.rand(2, 1, 5000 * C.PAGE, device="cuda")
+    before = t["weight"].double()
+    q = C.queries(2, n_q, group, d, dtype, seed=42)
+    o, lse = attend(sta, t, q, accumulate=True)
+    ok(sta)
+    want = [torch.zeros(2, n_q, group, d, dtype=torch.float64, device="cuda") for _ in range(2)]
+    want += [torch.zeros(2, group, n_q, dtype=torch.float64, device="cuda") for _ in range(2)]
+    added = torch.zeros_like(before)
+    for b in range(2):
+        pages = t["page_table"][b].long()
+        k = t["k_pages"][pages, 0].reshape(-1, d)[:n[b]].double()
+        v = t["v_pages"][pages, 0].reshape(-1, d)[:n[b]].double()
+        for i in range(n_q):
+            m = n[b] - (n_q - 1 - i)
+            x = q[b, i].double() @ k[:m].T * d ** -0.5
+            p = x.softmax(-1)
+            want[0][b, i], want[1][b, i] = p @ v[:m], p @ v[:m].abs()
+            want[2][b, :, i] = x.logsumexp(-1)
+            want[3][b, :, i] = (q[b, i].double().abs() @ k[:m].T.abs()).amax(-1) * d ** -0.5
+            added[b, 0, :m] += p.sum(0)
+    order = (0, 2, 1, 3)  # o, lse, sigma, terms
+    # additions one after another: at most 5000 / 148 pages of a CTA, 32 slots each, and the 148 parts
+    rel = C.check_attention(o, lse, [want[x].cpu().numpy() for x in order], d, dtype, 34 * 32 + 148)
+    limit = added * float(rel.max()) + (before + added) * (group * n_q + 1) * 2.0 ** -24
+    assert ((t["weight"].double() - before - added).abs() <= limit).all()
+
+
 def test_every_sequence_empty(sta):
     t = C.make([0, 0, 0], 2, 128, "fp16", seed=14)
     o, lse = compare(sta, t, C.queries(3, 2, 2, 128, "fp16", seed=14), "fp16", accumulate=True)

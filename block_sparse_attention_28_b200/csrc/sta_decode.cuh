@@ -6,17 +6,19 @@
 //
 // Every key and value is read once and used by the M <= 64 query rows of its
 // head: at most 64 flop per byte, so HBM bounds the call. The matrix products
-// are 16-row mma.sync tiles (a tcgen05 tile has at least 64 rows, of which a
-// token of a group of 1 to 8 heads would fill a few).
+// are mma.sync tiles with the keys (or the values' columns) along the 16 rows
+// and 8 query rows across: S^T = K Q^T, O^T = V^T P^T. (A tcgen05 tile has 64
+// rows at least; a token of a group of 1 to 8 heads has 8 to offer.)
 //
-// attend_kernel: one CTA per SM. The pages to be read are the units of work,
-// rows one after another, cut into one equal chunk per CTA whatever the
-// lengths are: no CTA waits for a long sequence. A producer warp streams pages
-// through a ring of shared memory (TMA, 128-byte swizzle). Eight warps take
-// them: two to a page (32 of its slots each), once for every 16 query rows, and
-// with fewer than 64 query rows two or four pages at a time. Each has a running
-// maximum and sum and its own output tile; they are merged where a row ends. Rows cut by a chunk border leave their parts (sum
-// relative to a maximum) in the workspace.
+// attend_kernel: one CTA per SM, 8 warps. A worker is a warp (two or four for
+// more than 16 or 32 query rows, 16 each) with a ring of its own in shared
+// memory, into which its first warp sends pieces of pages (TMA, 128-byte
+// swizzle) ahead of their use. The pages to be read, rows one after another,
+// are cut into one equal chunk per worker whatever the lengths are: no worker
+// waits for a long sequence, or for another where a row ends. Each warp keeps
+// the running maximum and sum and the outputs of its query rows in registers;
+// rows cut by a chunk border leave their parts (the sum relative to a maximum)
+// in the workspace.
 // join_kernel: joins those parts, and adds every slot's attention to its
 // weight once the row's log-sum-exp is known, from the scores that
 // attend_kernel left (4 bytes per slot and query row against 4 d for its key
@@ -33,29 +35,25 @@ namespace decode {
 using cache::Args;
 using cache::PAGE;
 
-constexpr int CONSUMERS = 8;  // warps
-constexpr int THREADS = 32 * (CONSUMERS + 1);
-constexpr int KEYS = PAGE / 2;  // slots of a page one warp takes
-constexpr int MAX_ROWS = 64;   // query rows per key head
 constexpr int MAX_CTAS = 148;  // one per SM of a B200
-constexpr int LEAST_UNITS = 1;
-constexpr int JOIN_THREADS = 256;
-constexpr int JOIN_SHARES = 8;  // CTAs of join_kernel for one of attend_kernel, when weights are added
+constexpr int WARPS = 8;
+constexpr int THREADS = 32 * WARPS;
+constexpr int MAX_ROWS = 64;  // query rows per key head
+constexpr int STAGE_BYTES = 8192;
+constexpr int RING_BYTES = 24 * STAGE_BYTES;  // of all workers
 constexpr long long DRAIN_LIMIT = 200000000LL;
+
+// Warps of a worker (16 query rows each) and workers of a CTA.
+__host__ __device__ inline int tiles_of(int M) { return M <= 16 ? 1 : (M <= 32 ? 2 : 4); }
+__host__ __device__ inline int workers_of(int M) { return WARPS / tiles_of(M); }
 
 template <int D>
 struct Cfg {
-  static constexpr int HALF_BYTES = PAGE * 128;           // 64 values of every token
-  static constexpr int TILE_BYTES = HALF_BYTES * (D / 64);  // keys or values of a page
-  static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
-  static constexpr int STAGES = 131072 / STAGE_BYTES;
-  // A warp waits for a stage's next load only after it has had the load before
-  // it, because page groups (4, 2 or 1) divide the stages: a barrier's phase
-  // parity is read one phase ahead at most.
-  static_assert(STAGES % 4 == 0, "page groups divide the stages");
-  static constexpr int MERGE_STRIDE = D + 8;  // floats; 8 more spread the rows over the banks
-  static constexpr int MERGE_BYTES = CONSUMERS * 16 * MERGE_STRIDE * 4;
-  static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + MERGE_BYTES;
+  static constexpr int KEYS = STAGE_BYTES / (4 * D);        // slots of a stage: 16 or 32
+  static constexpr int KT = KEYS / 16;
+  static constexpr int HALF_BYTES = KEYS * 128;             // 64 values of every slot
+  static constexpr int TILE_BYTES = HALF_BYTES * (D / 64);  // keys or values of a stage
+  static constexpr int SMEM = 1024 + RING_BYTES;
 };
 
 struct Shape {
@@ -65,20 +63,29 @@ struct Shape {
   float scale_log2;  // scale * log2 e
 };
 
-// A CTA's rows that it does not hold whole (row -1: none): [0] the one it
-// goes on with, [1] the one it begins.
+// A worker's rows that it does not hold whole (row -1: none): [0] the one it
+// goes on with, [1] the one it begins; the unit of the row's first page, and
+// its pages.
 struct Split {
-  int row[2], start[2], n[2];
+  int row[2], start[2], pages[2];
   int chunk, units;
 };
 
 struct Work {
-  float *part_o;      // [2 * MAX_CTAS][M][D]
-  float2 *part_ml;    // [2 * MAX_CTAS][M] maximum (log2) and sum
-  Split *split;       // [MAX_CTAS]
-  int2 *units;        // [units] (row, column of the page table or -1)
+  float *part_o;      // [2 * workers][M][D]
+  float2 *part_ml;    // [2 * workers][M] maximum (log2) and sum
+  Split *split;       // [workers]
+  int2 *units;        // [units] (row, column of the page table) of a page, else -1
   float *scores;      // [units][M][PAGE] s_j log2 e, -inf out of view
   float *lse2;        // [rows][M] log-sum-exp (log2) of the rows held whole
+};
+
+// What a worker's warps are told of a stage.
+enum : int { FIRST = 1, LAST = 2, WHOLE = 4, BEGINS = 8, SKIP = 16, END = 32, SUB_SHIFT = 8 };
+struct __align__(16) Piece {
+  int row, unit;
+  int held;   // filled slots from the piece's first on (may be above KEYS)
+  int flags;  // and, from SUB_SHIFT on, which piece of its page it is
 };
 
 // ------------------------------------------------------------ element types
@@ -135,6 +142,13 @@ __device__ __forceinline__ void ldmatrix_trans(uint32_t addr, uint32_t (&r)[4]) 
                : "r"(addr)
                : "memory");
 }
+// Transposes an 8 x 8 matrix of 2-byte elements held two to a register.
+__device__ __forceinline__ uint32_t transpose(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
+  return r;
+}
+
 // ------------------------------------------------------------------- rows
 struct RowPages {
   int len, n, first;  // length, pages attended to, first entry of its list
@@ -157,317 +171,341 @@ __device__ __forceinline__ RowPages row_pages(const Args &a, const Shape &s, int
   return p;
 }
 
-// A warp's view of 32 rows, one per lane, from row `base` on.
-struct Window {
-  int base;
-  RowPages mine;
-  __device__ __forceinline__ void load(const Args &a, const Shape &s, int from, int rows) {
-    base = from;
-    const int r = from + (int)(threadIdx.x & 31);
-    mine.len = mine.n = mine.first = 0;
-    if (r < rows) mine = row_pages(a, s, r);
+// --------------------------------------------------------------- producer
+// The first warp of a worker sends its pieces: 32 units at a time a lane each
+// finds its unit's row, column and page; the lanes then send them in order.
+template <int D>
+struct Producer {
+  using C = Cfg<D>;
+  uint8_t *ring;
+  uint64_t *full, *empty;
+  Piece *piece;
+  int stages;
+  int row, off;   // the next unit's row, units of the row before it
+  int u, u0, u1;  // the next unit, the worker's range
+  int issued;     // stages sent
+  bool ended, ok;
+  // this lane's unit of the batch at hand
+  int w_row, w_unit, w_held, w_flags, w_y;
+  unsigned left;  // lanes of the batch still to be sent
+  int sub;        // pieces of the first of them that are sent
+
+  // Looks up the next 32 units.
+  __device__ __forceinline__ void batch(const Args &a, const Shape &s, int rows, Split *split, int2 *units) {
+    static_assert(cache::ROW_COST == 1, "what is the worker's last page");
+    const int lane = threadIdx.x & 31;
+    const int r0 = row + lane;
+    RowPages mine = {0, 0, 0};
+    if (r0 < rows) mine = row_pages(a, s, r0);
+    const int upto = cache::warp_scan(cache::row_units(mine.n) - (lane == 0 ? off : 0));
+    const int total = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    const int take = min(min(total, u1 - u), 32);
+    int k = 0;  // the row of this lane's unit: the first with upto > lane
+#pragma unroll
+    for (int step = 16; step > 0; step >>= 1)
+      if (__shfl_sync(0xFFFFFFFFu, upto, k + step - 1) <= lane) k += step;
+    const int n = __shfl_sync(0xFFFFFFFFu, mine.n, k), first = __shfl_sync(0xFFFFFFFFu, mine.first, k);
+    const int len = __shfl_sync(0xFFFFFFFFu, mine.len, k), end = __shfl_sync(0xFFFFFFFFu, upto, k);
+    const int i = n - (end - lane);  // the row's i-th page; negative: the row's own unit
+    const bool page_unit = lane < take && i >= 0;
+    w_row = row + k;
+    w_unit = u + lane;
+    w_y = w_held = w_flags = 0;
+    int col = -1;
+    if (page_unit) {
+      const int b = w_row / a.H, h = w_row - b * a.H, start = w_unit - i;
+      col = i;
+      if (s.page_ptr != nullptr) {
+        col = s.page_idx[first + i];
+        if (!cache::column_ok(col, i > 0 ? s.page_idx[first + i - 1] : -1, cache::filled_pages(len))) {
+          record_error(DEV_ERR_BAD_MASK);
+          col = -1;
+        }
+      }
+      const int page = col >= 0 ? a.page(b, col * PAGE) : -1;
+      if (page >= 0) {
+        w_y = (page * a.H + h) * PAGE;
+        w_held = len - col * PAGE;
+      } else {
+        col = -1;
+        w_flags = SKIP;
+      }
+      const bool begins = start >= u0;
+      if (i == 0 || w_unit == u0) w_flags |= FIRST;
+      if (i == n - 1 || w_unit == u1 - 1) w_flags |= LAST;
+      // a row's own unit follows its last page, if anything does
+      if (w_unit == u1 - 1 || (i == n - 1 && w_unit == u1 - 2)) w_flags |= END;
+      if (begins) w_flags |= BEGINS;
+      if (begins && start + n <= u1) {
+        w_flags |= WHOLE;
+      } else if (w_flags & FIRST) {
+        split->row[begins] = w_row;
+        split->start[begins] = start;
+        split->pages[begins] = n;
+      }
+    }
+    if (units != nullptr && lane < take) units[w_unit] = page_unit ? make_int2(w_row, col) : make_int2(-1, -1);
+    left = __ballot_sync(0xFFFFFFFFu, page_unit);
+    sub = 0;
+    if (take > 0) {  // the unit after the batch
+      u += take;
+      const int lk = __shfl_sync(0xFFFFFFFFu, k, take - 1), le = __shfl_sync(0xFFFFFFFFu, end, take - 1);
+      const int ln = __shfl_sync(0xFFFFFFFFu, n, take - 1);
+      off = cache::row_units(ln) - (le - take);  // of row row + lk, its last unit included
+      row += lk;
+    } else {
+      row += 32;  // 32 rows without pages
+      off = 0;
+    }
+  }
+
+  // Sends the next piece.
+  __device__ __forceinline__ void send(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, const Shape &s,
+                                       int rows, Split *split, int2 *units, volatile uint32_t *abort,
+                                       long long limit) {
+    while (left == 0 && u < u1 && row < rows) batch(a, s, rows, split, units);
+    const int lane = threadIdx.x & 31, stage = issued % stages;
+    const bool none = left == 0;  // nothing but a row's own unit in the whole range
+    const int x = none ? 0 : __ffs(left) - 1;
+    int state = 0;
+    if (lane == x) {
+      const bool last = none || (w_flags & SKIP) || w_held <= (sub + 1) * C::KEYS || (sub + 1) * C::KEYS == PAGE;
+      int flags = none ? (SKIP | END) : w_flags | sub << SUB_SHIFT;
+      if (sub > 0) flags &= ~FIRST;
+      if (!last) flags &= ~(LAST | END);
+      if (issued < stages || tc::mbar_wait(&empty[stage], ((issued / stages) & 1) ^ 1, abort, limit)) {
+        piece[stage] = Piece{w_row, w_unit, w_held - sub * C::KEYS, flags};
+        if (flags & SKIP) {
+          tc::mbar_arrive(&full[stage]);
+        } else {
+          const uint32_t dst = tc::smem_u32(ring + stage * STAGE_BYTES);
+          const int y = w_y + sub * C::KEYS;
+          tc::mbar_expect_tx(&full[stage], STAGE_BYTES);
+#pragma unroll
+          for (int e = 0; e < D / 64; ++e) tc::tma_load_2d(dst + e * C::HALF_BYTES, &tk, &full[stage], 64 * e, y);
+#pragma unroll
+          for (int e = 0; e < D / 64; ++e)
+            tc::tma_load_2d(dst + C::TILE_BYTES + e * C::HALF_BYTES, &tv, &full[stage], 64 * e, y);
+        }
+        state = 1 | (last ? 2 : 0) | (flags & END);
+      }
+    }
+    state = __shfl_sync(0xFFFFFFFFu, state, x);
+    ok = state & 1;
+    ended = state & END;
+    if (ok) ++issued;
+    ++sub;
+    if (state & 2) {
+      sub = 0;
+      left &= left - 1;
+    }
   }
 };
-
-// --------------------------------------------------------------- producer
-// One warp: 32 units at a time, a lane each finds its unit's row, column and
-// page, then lane 0 issues the loads in order.
-template <int D>
-__device__ void produce(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, const Shape &s, int rows,
-                        int row, int off, int u, int u1, uint8_t *ring, uint64_t *full, uint64_t *empty,
-                        int *stage_col, volatile uint32_t *abort, long long limit) {
-  using C = Cfg<D>;
-  const int lane = threadIdx.x & 31;
-  int issued = 0;
-  bool ok = true;
-  while (u < u1 && row < rows && ok) {
-    Window w;
-    w.load(a, s, row, rows);
-    const int skip = lane == 0 ? off : 0;
-    const int upto = cache::warp_scan(w.mine.n - skip);  // units of the window up to this lane's row
-    const int total = __shfl_sync(0xFFFFFFFFu, upto, 31);
-    const int take = min(total, u1 - u);
-    for (int t0 = 0; t0 < take && ok; t0 += 32) {
-      const int t = t0 + lane;
-      int k = 0;  // first row of the window with upto > t
-#pragma unroll
-      for (int step = 16; step > 0; step >>= 1)
-        if (__shfl_sync(0xFFFFFFFFu, upto, k + step - 1) <= t) k += step;
-      k = min(k, 31);
-      const int n = __shfl_sync(0xFFFFFFFFu, w.mine.n, k), first = __shfl_sync(0xFFFFFFFFu, w.mine.first, k);
-      const int len = __shfl_sync(0xFFFFFFFFu, w.mine.len, k), end = __shfl_sync(0xFFFFFFFFu, upto, k);
-      const int r = row + k, b = r / a.H, h = r - b * a.H;
-      int col = -1, y = 0;
-      if (t < take) {
-        const int i = n - (end - t);  // the row's i-th page
-        col = i;
-        if (s.page_ptr != nullptr) {
-          col = s.page_idx[first + i];
-          if (!cache::column_ok(col, i > 0 ? s.page_idx[first + i - 1] : -1, cache::filled_pages(len))) {
-            record_error(DEV_ERR_BAD_MASK);
-            col = -1;
-          }
-        }
-        const int page = col >= 0 ? a.page(b, col * PAGE) : -1;
-        if (page < 0) col = -1;
-        y = page >= 0 ? (page * a.H + h) * PAGE : 0;
-      }
-      const int count = min(32, take - t0);
-      for (int x = 0; x < count && ok; ++x) {
-        const int xc = __shfl_sync(0xFFFFFFFFu, col, x), xy = __shfl_sync(0xFFFFFFFFu, y, x);
-        const int stage = issued % C::STAGES;
-        if (lane == 0) {
-          if (issued >= C::STAGES) ok = tc::mbar_wait(&empty[stage], ((issued / C::STAGES) & 1) ^ 1, abort, limit);
-          if (ok) {
-            stage_col[stage] = xc;
-            if (xc < 0) {
-              tc::mbar_arrive(&full[stage]);
-            } else {
-              const uint32_t dst = tc::smem_u32(ring + stage * C::STAGE_BYTES);
-              tc::mbar_expect_tx(&full[stage], C::STAGE_BYTES);
-#pragma unroll
-              for (int e = 0; e < D / 64; ++e) tc::tma_load_2d(dst + e * C::HALF_BYTES, &tk, &full[stage], 64 * e, xy);
-#pragma unroll
-              for (int e = 0; e < D / 64; ++e)
-                tc::tma_load_2d(dst + C::TILE_BYTES + e * C::HALF_BYTES, &tv, &full[stage], 64 * e, xy);
-            }
-          }
-        }
-        ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
-        if (ok) ++issued;
-      }
-    }
-    u += take;
-    row += 32;
-    off = 0;
-  }
-  // given up: the loads in flight still write to this CTA's shared memory
-  if (!ok && lane == 0)
-    for (int x = max(0, issued - C::STAGES); x < issued; ++x)
-      tc::mbar_wait(&full[x % C::STAGES], (x / C::STAGES) & 1, nullptr, DRAIN_LIMIT);
-}
-
-// Rows without any page: o = 0, lse = -inf. Row r is CTA r % CTAs'.
-template <int D, typename T>
-__device__ void fill_empty_rows(const Args &a, const Shape &s, int rows, T *o, float *lse) {
-  const int lane = threadIdx.x & 31;
-  const int M = s.group * s.n_q, heads = a.H * s.group;
-  for (long long r0 = blockIdx.x; r0 < rows; r0 += 32LL * gridDim.x) {
-    const long long mine = r0 + (long long)lane * gridDim.x;
-    const bool none = mine < rows && row_pages(a, s, (int)mine).n == 0;
-    for (unsigned left = __ballot_sync(0xFFFFFFFFu, none); left != 0; left &= left - 1) {
-      const int r = (int)(r0 + (long long)(__ffs(left) - 1) * gridDim.x);
-      const int b = r / a.H, h = r - b * a.H;
-      for (int e = lane; e < M * (D / 8); e += 32) {
-        const int m = e / (D / 8), i = m / s.group, g = m - i * s.group;
-        const long long row = ((long long)b * s.n_q + i) * heads + h * s.group + g;
-        reinterpret_cast<uint4 *>(o + row * D)[e % (D / 8)] = make_uint4(0u, 0u, 0u, 0u);
-      }
-      if (lse != nullptr)
-        for (int m = lane; m < M; m += 32) {
-          const int i = m / s.group, g = m - i * s.group;
-          lse[((long long)b * heads + h * s.group + g) * s.n_q + i] = -INFINITY;
-        }
-    }
-  }
-}
 
 // --------------------------------------------------------------- consumers
-// 16 query rows of one warp: thread (g, t) = (lane / 4, lane % 4) holds rows g
-// and g + 8 of the tile, columns 8 n + 2 t and + 1 of each 8-column piece n.
-template <int D>
+// 8 NT query rows of one warp. Thread (g, t) = (lane / 4, lane % 4) holds, of
+// query rows 8 n + 2 t + y (y = 0, 1): o[c][n][y + 2 x], their outputs
+// 16 c + g + 8 x; the running maximum (log2); its share of the sum.
+template <int D, int NT>
 struct Tile {
-  float o[D / 8][4];
-  float top[2], sum[2];  // running maximum (log2); this thread's share of the sum
+  float o[D / 16][NT][4];
+  float top[NT][2], sum[NT][2];
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
-    top[0] = top[1] = -INFINITY;
-    sum[0] = sum[1] = 0.0f;
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) o[c][n][0] = o[c][n][1] = o[c][n][2] = o[c][n][3] = 0.0f;
+      top[n][0] = top[n][1] = -INFINITY;
+      sum[n][0] = sum[n][1] = 0.0f;
+    }
   }
 };
 
-// Query rows of tile mt as the A operand of D / 16 steps (rows past M: zero).
-template <int D, typename T>
-__device__ __forceinline__ void load_queries(const T *q, const Args &a, const Shape &s, int b, int h, int mt,
-                                             uint32_t (&qa)[D / 16][4]) {
+// Query rows m0 .. m0 + 8 NT - 1 as the B operand of D / 16 steps (rows past M:
+// zero).
+template <int D, int NT, typename T>
+__device__ __forceinline__ void load_queries(const T *q, const Args &a, const Shape &s, int r, int m0,
+                                             uint32_t (&qb)[NT][D / 16][2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int b = r / a.H, h = r - b * a.H;
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int m = mt * 16 + g + 8 * half;
+  for (int n = 0; n < NT; ++n) {
+    const int m = m0 + 8 * n + g;
     const bool in = m < s.group * s.n_q;
     const int i = in ? m / s.group : 0, hg = in ? m - i * s.group : 0;
     const uint32_t *row = reinterpret_cast<const uint32_t *>(
         q + (((long long)b * s.n_q + i) * (a.H * s.group) + h * s.group + hg) * D);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-      qa[ks][half] = in ? row[ks * 8 + t] : 0u;
-      qa[ks][2 + half] = in ? row[ks * 8 + 4 + t] : 0u;
+      qb[n][ks][0] = in ? row[ks * 8 + t] : 0u;
+      qb[n][ks][1] = in ? row[ks * 8 + 4 + t] : 0u;
     }
   }
 }
 
-// KEYS slots of a page (kt, vt: where their keys and values begin): scores, softmax step, weighted
-// values. lim[x]: how many of them row g + 8 x sees; held: how many are filled
-// (either may be negative or above KEYS). edge: any of these is below KEYS.
-// scores: where this tile's scores go (MASS), of which it has `rows` rows.
-template <int D, typename T, bool MASS>
-__device__ __forceinline__ void attend_slots(uint32_t kt, uint32_t vt, const uint32_t (&qa)[D / 16][4],
-                                             const Shape &s, const int (&lim)[2], int held, bool edge, Tile<D> &acc,
-                                             float *scores, int rows) {
+// One stage (its keys at kt, its values at vt): scores, softmax step, weighted
+// values. lim[n][y]: how many of its slots query row 8 n + 2 t + y sees; held:
+// how many are filled (either may be negative or above KEYS). edge: any of
+// these is below KEYS. scores: where query row 0's scores go (MASS), of which
+// the warp has `rows` rows.
+template <int D, int NT, typename T, bool MASS>
+__device__ __forceinline__ void attend_slots(uint32_t kt, uint32_t vt, const uint32_t (&qb)[NT][D / 16][2],
+                                             const Shape &s, const int (&lim)[NT][2], int held, bool edge,
+                                             Tile<D, NT> &acc, float *scores, int rows) {
   using N = Num<T>;
-  constexpr int HALF_BYTES = Cfg<D>::HALF_BYTES;
+  using C = Cfg<D>;
+  constexpr int KT = C::KT;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  float p[KEYS / 8][4];
+  // ldmatrix addresses: lane -> (row lane % 8 of matrix lane / 8)
+  const int l7 = lane & 7, m8 = lane >> 3;
+  float p[KT][NT][4];
   {
-    const uint32_t row = kt + (lane & 7) * 128, x = lane & 7, m = lane >> 3;
+    // A = K: matrices (slots 0..7, 8..15) x (16-byte pieces 2 ks, 2 ks + 1).
+    // Two chains of additions each for the even and the odd steps.
+    float odd_p[KT][NT][4];
+    const uint32_t row = kt + (l7 + (m8 & 1) * 8) * 128;
 #pragma unroll
-    for (int n = 0; n < KEYS / 8; ++n) {
-      p[n][0] = p[n][1] = p[n][2] = p[n][3] = 0.0f;
+    for (int x = 0; x < KT; ++x)
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        uint32_t kb[4];
-        // 16-byte pieces 4 j .. 4 j + 3 of keys 8 n .. 8 n + 7
-        ldmatrix(row + n * 1024 + (j >> 1) * HALF_BYTES + ((((j & 1) * 4 + m) ^ x) << 4), kb);
-        N::mma(p[n], qa[2 * j], kb[0], kb[1]);
-        N::mma(p[n], qa[2 * j + 1], kb[2], kb[3]);
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[x][n][e] = odd_p[x][n][e] = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+      for (int x = 0; x < KT; ++x) {
+        uint32_t ka[4];
+        ldmatrix(row + x * 2048 + (ks >> 2) * C::HALF_BYTES + ((((ks & 3) * 2 + (m8 >> 1)) ^ l7) << 4), ka);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) N::mma(ks & 1 ? odd_p[x][n] : p[x][n], ka, qb[n][ks][0], qb[n][ks][1]);
       }
-    }
+#pragma unroll
+    for (int x = 0; x < KT; ++x)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[x][n][e] = (p[x][n][e] + odd_p[x][n][e]) * s.scale_log2;
+          if (edge && 16 * x + g + 8 * (e >> 1) >= lim[n][e & 1]) p[x][n][e] = -INFINITY;
+        }
   }
-#pragma unroll
-  for (int n = 0; n < KEYS / 8; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      p[n][e] *= s.scale_log2;
-      if (edge && 8 * n + 2 * t + (e & 1) >= lim[e >> 1]) p[n][e] = -INFINITY;
-    }
   if (MASS) {
 #pragma unroll
-    for (int n = 0; n < KEYS / 8; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (g + 8 * x < rows)
-          *reinterpret_cast<float2 *>(scores + (g + 8 * x) * PAGE + 8 * n + 2 * t) =
-              make_float2(p[n][2 * x], p[n][2 * x + 1]);
+      for (int e = 0; e < 4; ++e)
+        if (const int m = 8 * n + 2 * t + (e & 1); m < rows)
+#pragma unroll
+          for (int x = 0; x < KT; ++x) scores[m * PAGE + 16 * x + g + 8 * (e >> 1)] = p[x][n][e];
   }
-  float base[2], keep[2];
+  float keep[NT][2];
+  bool grown = false;
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    float up = -INFINITY;
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int n = 0; n < KEYS / 8; ++n) up = tc::fmax3(up, p[n][2 * x], p[n][2 * x + 1]);
-    up = fmaxf(up, __shfl_xor_sync(0xFFFFFFFFu, up, 1));
-    up = fmaxf(up, __shfl_xor_sync(0xFFFFFFFFu, up, 2));
-    up = fmaxf(up, acc.top[x]);
-    const float from = up == -INFINITY ? 0.0f : up;  // a row that has seen nothing yet
-    keep[x] = tc::ex2(acc.top[x] - from);
-    acc.top[x] = up;
-    base[x] = from - N::SHIFT;
-  }
-  if (__any_sync(0xFFFFFFFFu, keep[0] != 1.0f || keep[1] != 1.0f)) {
+    for (int y = 0; y < 2; ++y) {
+      float up = acc.top[n][y];
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n) {
-      acc.o[n][0] *= keep[0];
-      acc.o[n][1] *= keep[0];
-      acc.o[n][2] *= keep[1];
-      acc.o[n][3] *= keep[1];
-    }
-  }
+      for (int x = 0; x < KT; ++x) up = tc::fmax3(up, p[x][n][y], p[x][n][y + 2]);
+      up = fmaxf(up, __shfl_xor_sync(0xFFFFFFFFu, up, 4));
+      up = fmaxf(up, __shfl_xor_sync(0xFFFFFFFFu, up, 8));
+      up = fmaxf(up, __shfl_xor_sync(0xFFFFFFFFu, up, 16));
+      const float from = up == -INFINITY ? 0.0f : up;  // a row that has seen nothing yet
+      keep[n][y] = tc::ex2(acc.top[n][y] - from);
+      grown |= keep[n][y] != 1.0f;
+      acc.top[n][y] = up;
+      const float base = from - N::SHIFT;
+      float z = 0.0f;
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    float z = 0.0f;
-#pragma unroll
-    for (int n = 0; n < KEYS / 8; ++n)
-#pragma unroll
-      for (int e = 2 * x; e < 2 * x + 2; ++e) {
-        p[n][e] = tc::ex2(p[n][e] - base[x]);
-        z += p[n][e];
+      for (int x = 0; x < KT; ++x) {
+        p[x][n][y] = tc::ex2(p[x][n][y] - base);
+        p[x][n][y + 2] = tc::ex2(p[x][n][y + 2] - base);
+        z += p[x][n][y] + p[x][n][y + 2];
       }
-    acc.sum[x] = acc.sum[x] * keep[x] + z;
-  }
-  // The weights of slots 16 ks .. 16 ks + 15 as the A operand, split in two
-  // terms: one alone would be off by as much as the output's own rounding.
-  auto weights = [&](int ks, uint32_t(&hi)[4], uint32_t(&lo)[4]) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float p0 = p[2 * ks + (e >> 1)][(e & 1) * 2], p1 = p[2 * ks + (e >> 1)][(e & 1) * 2 + 1];
-      hi[e] = N::pack(p0, p1);
-      const float2 r = N::unpack(hi[e]);
-      lo[e] = N::pack(p0 - r.x, p1 - r.y);
+      acc.sum[n][y] = acc.sum[n][y] * keep[n][y] + z;
     }
-  };
-  const uint32_t vrow = vt + ((lane & 7) + ((lane >> 3) & 1) * 8) * 128, vx = lane & 7, vc = lane >> 4;
+  if (__any_sync(0xFFFFFFFFu, grown)) {
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc.o[c][n][e] *= keep[n][e & 1];
+  }
   // Values of slots that are not seen must not reach the products even with a
-  // weight of 0 (0 * inf): registers of slots >= held are cleared. A slot that
-  // only the newer of the n_q tokens see is cleared where it is not finite,
-  // and what is not finite added by hand for those who see it.
-  auto slots_below = [&](int key, int upto) { return key + 1 < upto ? 0xFFFFFFFFu : (key < upto ? 0xFFFFu : 0u); };
+  // weight of 0 (0 * inf): those of slots >= held are cleared. A slot that only
+  // the newer of the n_q tokens see is cleared where it is not finite, and what
+  // is not finite added by hand for those who see it.
+  auto slots_below = [&](int key) { return key + 1 < held ? 0xFFFFFFFFu : (key < held ? 0xFFFFu : 0u); };
   auto finite = [](uint32_t v) {
     return ((v & N::NONFINITE) == N::NONFINITE ? 0u : v & 0xFFFFu) |
            ((v >> 16 & N::NONFINITE) == N::NONFINITE ? 0u : v & 0xFFFF0000u);
   };
-  auto value_pair = [&](int key, int c) {  // values 8 c + 2 t and + 1
+  auto value = [&](int key, int d) {  // of slot `key`, in the low half
     uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];"
+    asm volatile("ld.shared.u16 %0, [%1];"
                  : "=r"(v)
-                 : "r"(vt + (c >> 3) * HALF_BYTES + key * 128 + (((c & 7) ^ (key & 7)) << 4) + 4 * t));
+                 : "r"(vt + (d >> 6) * C::HALF_BYTES + key * 128 + ((((d & 63) >> 3) ^ (key & 7)) << 4) + (d & 7) * 2));
     return v;
   };
   bool odd = false;
   if (edge && s.n_q > 1) {
-    for (int key = max(0, held - (s.n_q - 1)) + g; key < min(KEYS, held); key += 8)
-      for (int c = 0; c < D / 8; ++c) {
-        const uint32_t v = value_pair(key, c);
-        odd |= finite(v) != v;
-      }
+    for (int key = max(0, held - (s.n_q - 1)); key < min(C::KEYS, held); ++key)
+      for (int d = lane; d < D; d += 32) odd |= (value(key, d) & N::NONFINITE) == N::NONFINITE;
     odd = __any_sync(0xFFFFFFFFu, odd);
   }
 #pragma unroll
-  for (int ks = 0; ks < KEYS / 16; ++ks) {
-    // the weights of slots 16 ks .. 16 ks + 15 as the A operand, split in two
-    // terms: one alone would be off by as much as the output's own rounding
-    uint32_t hi[4], lo[4];
+  for (int x = 0; x < KT; ++x) {
+    // the weights of 16 slots as the B operand, split in two terms: one alone
+    // would be off by as much as the output's own rounding
+    uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float p0 = p[2 * ks + (e >> 1)][(e & 1) * 2], p1 = p[2 * ks + (e >> 1)][(e & 1) * 2 + 1];
-      hi[e] = N::pack(p0, p1);
-      const float2 r = N::unpack(hi[e]);
-      lo[e] = N::pack(p0 - r.x, p1 - r.y);
-    }
-    const uint32_t m0 = slots_below(16 * ks + 2 * t, held), m1 = slots_below(16 * ks + 8 + 2 * t, held);
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int c = 0; c < D / 8; c += 2) {
-      uint32_t vb[4];
-      // keys 16 ks .. 16 ks + 15, 16-byte pieces c and c + 1
-      ldmatrix_trans(vrow + ks * 2048 + (c >> 3) * HALF_BYTES + ((((c & 7) + vc) ^ vx) << 4), vb);
+      for (int e = 0; e < 2; ++e) {
+        const float p0 = p[x][n][2 * e], p1 = p[x][n][2 * e + 1];
+        const uint32_t v = N::pack(p0, p1);
+        const float2 r = N::unpack(v);
+        hi[n][e] = transpose(v);
+        lo[n][e] = transpose(N::pack(p0 - r.x, p1 - r.y));
+      }
+    // A = V^T: matrices (16-byte pieces 2 c, 2 c + 1) x (slots 0..7, 8..15)
+    const uint32_t row = vt + (x * 16 + l7 + (m8 >> 1) * 8) * 128;
+    const uint32_t m0 = slots_below(16 * x + 2 * t), m1 = slots_below(16 * x + 8 + 2 * t);
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      uint32_t va[4];
+      ldmatrix_trans(row + (c >> 2) * C::HALF_BYTES + ((((c & 3) * 2 + (m8 & 1)) ^ l7) << 4), va);
       if (edge) {
-        vb[0] &= m0;
-        vb[1] &= m1;
-        vb[2] &= m0;
-        vb[3] &= m1;
+        va[0] &= m0;
+        va[1] &= m0;
+        va[2] &= m1;
+        va[3] &= m1;
         if (odd) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) vb[e] = finite(vb[e]);
+          for (int e = 0; e < 4; ++e) va[e] = finite(va[e]);
         }
       }
-      N::mma(acc.o[c], hi, vb[0], vb[1]);
-      N::mma(acc.o[c + 1], hi, vb[2], vb[3]);
-      N::mma(acc.o[c], lo, vb[0], vb[1]);
-      N::mma(acc.o[c + 1], lo, vb[2], vb[3]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) N::mma(acc.o[c][n], va, hi[n][0], hi[n][1]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) N::mma(acc.o[c][n], va, lo[n][0], lo[n][1]);
     }
   }
   if (odd)
-    for (int key = 0; key < min(KEYS, held); ++key)
+    for (int key = 0; key < min(C::KEYS, held); ++key)
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint32_t v = value_pair(key, c);
-        const uint32_t bad = v ^ finite(v);  // the halves that are not finite, as they are
-        const float2 x = N::unpack(bad);
-        if (bad != 0)
+      for (int c = 0; c < D / 16; ++c)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (key < lim[e >> 1]) acc.o[c][e] += e & 1 ? x.y : x.x;
-      }
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t v = value(key, 16 * c + g + 8 * x);
+          if ((v & N::NONFINITE) == N::NONFINITE)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                if (key < lim[n][y]) acc.o[c][n][y + 2 * x] += N::unpack(v).x;
+        }
 }
 
 // Where row m of row r's result goes.
@@ -479,6 +517,14 @@ struct Sink {
     const int b = r / a.H, h = r - b * a.H, i = m / s.group, g = m - i * s.group;
     return ((long long)b * s.n_q + i) * (a.H * s.group) + h * s.group + g;
   }
+  // a row that sees nothing: o = 0, lse = -inf (one thread)
+  __device__ __forceinline__ void put_nothing(const Args &a, const Shape &s, int r) const {
+    for (int m = 0; m < s.group * s.n_q; ++m) {
+      for (int c = 0; c < D / 8; ++c)
+        reinterpret_cast<uint4 *>(o + row(a, s, r, m) * D)[c] = make_uint4(0u, 0u, 0u, 0u);
+      put_lse(a, s, r, m, -INFINITY);
+    }
+  }
   // y: log-sum-exp (log2)
   __device__ __forceinline__ void put_lse(const Args &a, const Shape &s, int r, int m, float y) const {
     const int b = r / a.H, h = r - b * a.H, i = m / s.group, g = m - i * s.group;
@@ -487,278 +533,323 @@ struct Sink {
   }
 };
 
-template <int D, typename T, bool MASS>
+template <int D, int NT, typename T, bool MASS>
 __global__ void __launch_bounds__(THREADS, 1)
 attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const Args a,
               const Shape s, const T *__restrict__ q, const Sink<D, T> sink, const Work work, long long limit) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
-  __shared__ int stage_col[C::STAGES];
-  __shared__ float2 merge_ml[CONSUMERS][16];
-  __shared__ int warp_units[CONSUMERS + 1];
-  __shared__ int begin[2];  // row and page of it that this CTA begins with
+  constexpr int STAGES = RING_BYTES / STAGE_BYTES;
+  __shared__ uint64_t full[STAGES], empty[STAGES];  // worker after worker
+  __shared__ Piece pieces[STAGES];
+  __shared__ int warp_units[WARPS];
+  __shared__ int begin[WARPS][2];  // row each worker begins in, units of it before
   __shared__ uint32_t abort;
-  uint8_t *ring = smem_raw + (1024 - (tc::smem_u32(smem_raw) & 1023u));
-  float *merge = reinterpret_cast<float *>(ring + C::STAGES * C::STAGE_BYTES);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rows = a.B * a.H, M = s.group * s.n_q;
-  // two warps per page and 16 query rows; the rest side by side over the pages
-  const int tiles = M <= 16 ? 1 : (M <= 32 ? 2 : 4), groups = CONSUMERS / (2 * tiles);
+  const int tiles = tiles_of(M), workers = workers_of(M), stages = STAGES / workers;
+  const int wk = warp / tiles, mt = warp % tiles, g = lane >> 2, t = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid == 0) {
-    for (int i = 0; i < C::STAGES; ++i) {
-      tc::mbar_init(&full[i], 1);
-      tc::mbar_init(&empty[i], 2 * tiles);
-    }
-    abort = 0u;
+  if (tid < STAGES) {
+    tc::mbar_init(&full[tid], 1);
+    tc::mbar_init(&empty[tid], tiles);
     tc::fence_barrier_init();
   }
-  // units before each thread's rows
+  if (tid == 0) abort = 0u;
+  // units before each thread's rows; rows without pages get their zeros here
   const int per = (rows + THREADS - 1) / THREADS;
   const int lo = (int)min((long long)rows, (long long)tid * per), hi = min(rows, lo + per);
   int mine = 0;
-  for (int r = lo; r < hi; ++r) mine += row_pages(a, s, r).n;
+  for (int r = lo; r < hi; ++r) {
+    const int n = row_pages(a, s, r).n;
+    mine += cache::row_units(n);
+    if (n == 0 && r % gridDim.x == blockIdx.x) sink.put_nothing(a, s, r);
+  }
   const int upto = cache::warp_scan(mine);
   if (lane == 31) warp_units[warp] = upto;
   __syncthreads();
   int units = 0, before = upto - mine;
 #pragma unroll
-  for (int w = 0; w < CONSUMERS + 1; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w < warp) before += warp_units[w];
     units += warp_units[w];
   }
-  const int chunk = cache::chunk_units(units, gridDim.x, LEAST_UNITS);
-  const int u0 = cache::chunk_begin(blockIdx.x, chunk, units), u1 = cache::chunk_begin(blockIdx.x + 1, chunk, units);
-  if (u0 < u1 && before <= u0 && u0 < before + mine) {
-    int at = before, r = lo;
-    for (; r < hi; ++r) {
-      const int n = row_pages(a, s, r).n;
-      if (u0 < at + n) break;
-      at += n;
+  // few units: a worker of every SM before a second one of any
+  const int chunk = cache::chunk_units(units, workers * gridDim.x);
+  for (int w = 0; w < workers; ++w) {
+    const int u0 = cache::chunk_begin(w * gridDim.x + blockIdx.x, chunk, units);
+    if (u0 < units && before <= u0 && u0 < before + mine) {
+      int at = before, r = lo;
+      for (; r < hi; ++r) {
+        const int n = cache::row_units(row_pages(a, s, r).n);
+        if (u0 < at + n) break;
+        at += n;
+      }
+      begin[w][0] = r;
+      begin[w][1] = u0 - at;
     }
-    begin[0] = r;
-    begin[1] = u0 - at;
   }
   __syncthreads();
-  if (warp == CONSUMERS) {
-    if (u0 < u1)
-      produce<D>(tk, tv, a, s, rows, begin[0], begin[1], u0, u1, ring, full, empty, stage_col, &abort, limit);
-    fill_empty_rows<D, T>(a, s, rows, sink.o, sink.lse);
-    return;
+  const int worker = wk * gridDim.x + blockIdx.x;
+  const int u0 = cache::chunk_begin(worker, chunk, units), u1 = cache::chunk_begin(worker + 1, chunk, units);
+  Split *split = work.split + worker;
+  if (mt == 0 && lane == 0) {
+    split->row[0] = split->row[1] = -1;
+    split->chunk = chunk;
+    split->units = units;
   }
+  __syncwarp();
+  if (u0 >= u1) return;
 
-  Split split;
-  split.row[0] = split.row[1] = -1;
-  split.start[0] = split.start[1] = split.n[0] = split.n[1] = 0;
-  split.chunk = chunk;
-  split.units = units;
-  const int mt = warp % tiles, pg = warp / tiles / 2, g = lane >> 2, t = lane & 3;
-  const int key0 = warp / tiles % 2 * KEYS;
-  const int tile_rows = min(16, M - 16 * mt);  // may be <= 0
-  int u = u0, row = u0 < u1 ? begin[0] : 0, off = u0 < u1 ? begin[1] : 0;
-  int done = 0;  // units of this CTA before the row's
+  Producer<D> p;
+  p.ring = smem_raw + (1024 - (tc::smem_u32(smem_raw) & 1023u)) + wk * stages * STAGE_BYTES;
+  p.full = full + wk * stages;
+  p.empty = empty + wk * stages;
+  p.piece = pieces + wk * stages;
+  p.stages = stages;
+  p.row = begin[wk][0];
+  p.off = begin[wk][1];
+  p.u = p.u0 = u0;
+  p.u1 = u1;
+  p.issued = p.sub = 0;
+  p.ended = false;
+  p.ok = true;
+  p.left = 0;
+  const int m0 = 16 * mt, tile_rows = min(8 * NT, M - m0);  // may be <= 0
+  int back[NT][2];  // newer tokens than the query row's
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int m = m0 + 8 * n + 2 * t + y;
+      back[n][y] = m < M ? s.n_q - 1 - m / s.group : 0;
+    }
   bool ok = true;
-  bool pending = false;  // a merge that all warps read may still be being read
-  Window win;
-  if (u0 < u1) win.load(a, s, row, rows);
-  Tile<D> acc;
-  while (u < u1 && row < rows) {
-    // next row with pages left
-    const unsigned has = __ballot_sync(0xFFFFFFFFu, win.mine.n > (win.base + lane == row ? off : 0) &&
-                                                        win.base + lane >= row);
-    if (has == 0) {
-      row = win.base + 32;
-      off = 0;
-      win.load(a, s, row, rows);
-      continue;
+  Tile<D, NT> acc;
+  uint32_t qb[NT][D / 16][2];
+  int stage = 0, parity = 0;
+  for (int it = 0;; ++it) {
+    if (mt == 0)
+      while (p.ok && !p.ended && p.issued < it + stages)
+        p.send(tk, tv, a, s, rows, split, MASS ? work.units : nullptr, &abort, limit);
+    ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&p.full[stage], parity, &abort, limit));
+    if (!ok) break;
+    const Piece d = p.piece[stage];
+    if (d.flags & FIRST) {
+      load_queries<D, NT, T>(q, a, s, d.row, m0, qb);
+      acc.clear();
     }
-    const int k = __ffs(has) - 1;
-    if (win.base + k != row) off = 0;
-    row = win.base + k;
-    const int n = __shfl_sync(0xFFFFFFFFu, win.mine.n, k), len = __shfl_sync(0xFFFFFFFFu, win.mine.len, k);
-    const int seg = min(n - off, u1 - u);
-    const int b = row / a.H, h = row - b * a.H;
-    const bool whole = off == 0 && seg == n;
-    if (!whole) {
-      const int x = off > 0 ? 0 : 1;
-      split.row[x] = row;
-      split.start[x] = u - off;
-      split.n[x] = n;
-    }
-    acc.clear();
-    const int lead = (pg - done % groups + groups) % groups;  // this warp's first page of the row
-    const bool active = lead < seg && tile_rows > 0;
-    if (lead < seg) {
-      uint32_t qa[D / 16][4];
-      load_queries<D, T>(q, a, s, b, h, mt, qa);
-      const int m0 = 16 * mt + g, m1 = m0 + 8;
-      const int back0 = m0 < M ? s.n_q - 1 - m0 / s.group : 0, back1 = m1 < M ? s.n_q - 1 - m1 / s.group : 0;
-      for (int x = lead; x < seg; x += groups) {
-        const int it = done + x, stage = it % C::STAGES;
-        if (ok) ok = tc::mbar_wait(&full[stage], (it / C::STAGES) & 1, &abort, limit);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        const int col = ok ? stage_col[stage] : -1;
-        if (MASS && lane == 0 && mt == 0 && key0 == 0) work.units[u + x] = make_int2(row, col);
-        if (col >= 0 && tile_rows > 0) {
-          const int held = len - col * PAGE - key0;
-          const int lim[2] = {held - back0, held - back1};
-          const uint32_t kt = tc::smem_u32(ring + stage * C::STAGE_BYTES) + key0 * 128;
-          float *sc = MASS ? work.scores + ((long long)(u + x) * M + 16 * mt) * PAGE + key0 : nullptr;
-          attend_slots<D, T, MASS>(kt, kt + C::TILE_BYTES, qa, s, lim, held, held - (s.n_q - 1) < KEYS, acc, sc,
+    if (!(d.flags & SKIP) && tile_rows > 0) {
+      int lim[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) lim[n][y] = d.held - back[n][y];
+      const uint32_t kt = tc::smem_u32(p.ring + stage * STAGE_BYTES);
+      float *sc = nullptr;
+      if (MASS) sc = work.scores + ((long long)d.unit * M + m0) * PAGE + (d.flags >> SUB_SHIFT) * C::KEYS;
+      attend_slots<D, NT, T, MASS>(kt, kt + C::TILE_BYTES, qb, s, lim, d.held, d.held - (s.n_q - 1) < C::KEYS, acc, sc,
                                    tile_rows);
-        }
-        __syncwarp();
-        if (lane == 0 && ok) tc::mbar_arrive(&empty[stage]);
-      }
     }
-    // the row's sum in this thread's rows
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      acc.sum[x] += __shfl_xor_sync(0xFFFFFFFFu, acc.sum[x], 1);
-      acc.sum[x] += __shfl_xor_sync(0xFFFFFFFFu, acc.sum[x], 2);
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&p.empty[stage]);
+    if (++stage == stages) {
+      stage = 0;
+      parity ^= 1;
     }
-    const int part = cache::part_of(blockIdx.x, off);
-    auto put = [&](int m, int d, float o0, float o1, float top, float sum) {
-      // two neighbouring outputs of query row m
-      if (whole) {
-        const float z = sum == 0.0f ? 0.0f : 1.0f / sum;
-        *reinterpret_cast<uint32_t *>(sink.o + sink.row(a, s, row, m) * D + d) = Num<T>::pack(o0 * z, o1 * z);
-        if (d == 0) {
-          const float y = sum == 0.0f ? -INFINITY : top + log2f(sum);
-          sink.put_lse(a, s, row, m, y);
-          if (MASS) work.lse2[(long long)row * M + m] = y;
-        }
-      } else {
-        *reinterpret_cast<float2 *>(work.part_o + ((long long)part * M + m) * D + d) = make_float2(o0, o1);
-        if (d == 0) work.part_ml[(long long)part * M + m] = make_float2(top, sum);
-      }
-    };
-    // The parts go through shared memory: one is written when the merge before
-    // has been read, and read when all are written. All warps take part, or,
-    // where the row has a single page here, that page's.
-    auto everyone = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * CONSUMERS) : "memory"); };
-    auto page_warps = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(2 + pg), "r"(64 * tiles) : "memory"); };
-    if (seg > 1 || pending) everyone();
-    pending = seg > 1;
-    if (seg > 1 || lead == 0) {
-      if (seg == 1) page_warps();
-      if (active) {
+    if (d.flags & LAST) {
+      const long long part = (long long)cache::part_of(worker, d.flags & BEGINS) * M + m0;
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (g + 8 * x < tile_rows) {
-            float *to = merge + (warp * 16 + g + 8 * x) * C::MERGE_STRIDE + 2 * t;
+      for (int n = 0; n < NT; ++n) {
+        float scale[2];
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-              *reinterpret_cast<float2 *>(to + 8 * c) = make_float2(acc.o[c][2 * x], acc.o[c][2 * x + 1]);
-            if (t == 0) merge_ml[warp][g + 8 * x] = make_float2(acc.top[x], acc.sum[x]);
+        for (int y = 0; y < 2; ++y) {
+          float sum = acc.sum[n][y];
+          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
+          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
+          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+          const float top = (acc.top[n][y] == -INFINITY ? 0.0f : acc.top[n][y]) - Num<T>::SHIFT;
+          scale[y] = sum == 0.0f ? 0.0f : 1.0f / sum;
+          const int m = 8 * n + 2 * t + y;
+          if (g == 0 && m < tile_rows) {
+            if (d.flags & WHOLE) {
+              const float lse2 = sum == 0.0f ? -INFINITY : top + log2f(sum);
+              sink.put_lse(a, s, d.row, m0 + m, lse2);
+              if (MASS) work.lse2[(long long)d.row * M + m0 + m] = lse2;
+            } else {
+              work.part_ml[part + m] = make_float2(top, sum);
+            }
           }
-      }
-      if (seg == 1)
-        page_warps();
-      else
-        everyone();
-      const int from = done % groups, have = min(groups, seg);  // page groups that hold a part
-      const int threads = seg == 1 ? 64 * tiles : 32 * CONSUMERS;
-      for (int e = seg == 1 ? tid - pg * 64 * tiles : tid; e < M * (D / 2); e += threads) {
-        const int m = e / (D / 2), d = e % (D / 2) * 2;
-        const int wt = m >> 4, wr = m & 15;
-        auto holder = [&](int x) { return ((from + (x >> 1)) % groups * 2 + (x & 1)) * tiles + wt; };
-        float top = -INFINITY;
-        for (int x = 0; x < 2 * have; ++x) top = fmaxf(top, merge_ml[holder(x)][wr].x);
-        const float at = top == -INFINITY ? 0.0f : top;
-        float sum = 0.0f, o0 = 0.0f, o1 = 0.0f;
-        for (int x = 0; x < 2 * have; ++x) {
-          const int w = holder(x);
-          const float2 ml = merge_ml[w][wr];
-          const float f = tc::ex2(ml.x - at);
-          const float2 v = *reinterpret_cast<const float2 *>(merge + (w * 16 + wr) * C::MERGE_STRIDE + d);
-          sum += ml.y * f;
-          o0 += v.x * f;
-          o1 += v.y * f;
         }
-        put(m, d, o0, o1, at - Num<T>::SHIFT, sum);
+        if (d.flags & WHOLE) {
+          const int m = 8 * n + g;
+          T *to = sink.o + (m < tile_rows ? sink.row(a, s, d.row, m0 + m) : 0) * D + 2 * t;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t v =
+                  transpose(Num<T>::pack(acc.o[c][n][2 * x] * scale[0], acc.o[c][n][2 * x + 1] * scale[1]));
+              if (m < tile_rows) *reinterpret_cast<uint32_t *>(to + 16 * c + 8 * x) = v;
+            }
+        } else {
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            if (const int m = 8 * n + 2 * t + y; m < tile_rows)
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                  work.part_o[(part + m) * D + 16 * c + g + 8 * x] = acc.o[c][n][y + 2 * x];
+        }
       }
     }
-    done += seg;
-    u += seg;
-    off += seg;
-    if (off == n) {
-      ++row;
-      off = 0;
-      if (row >= win.base + 32 && u < u1) win.load(a, s, row, rows);
-    }
+    if (d.flags & END) break;
   }
-  if (tid == 0) work.split[blockIdx.x] = split;
+  // given up: the loads in flight still write to this CTA's shared memory
+  if (mt == 0 && lane == 0 && !(ok && p.ok))
+    for (int x = max(0, p.issued - stages); x < p.issued; ++x)
+      tc::mbar_wait(&p.full[x % stages], (x / stages) & 1, nullptr, DRAIN_LIMIT);
 }
 
-// grid.x = the CTAs of attend_kernel, grid.y shares out each one's units.
+// grid.x = the workers of attend_kernel; grid.y shares out each one's units.
+constexpr int JOIN_THREADS = 128;
+constexpr int JOIN_SHARES = 4;
+
+// (maximum, sum) of two parts of a sum of exponentials; a sum of 0 is nothing.
+__device__ __forceinline__ float2 join_two(float2 x, float2 y) {
+  if (y.y == 0.0f) return x;
+  if (x.y == 0.0f) return y;
+  const float top = fmaxf(x.x, y.x);
+  return make_float2(top, x.y * tc::ex2(x.x - top) + y.y * tc::ex2(y.x - top));
+}
+
 template <int D, typename T, bool MASS>
 __global__ void __launch_bounds__(JOIN_THREADS)
 join_kernel(const Args a, const Shape s, const Sink<D, T> sink, const Work work) {
-  extern __shared__ float factor[];  // [parts][M]
+  constexpr int W = JOIN_THREADS / 32;
   __shared__ float row_lse[2][MAX_ROWS];
+  __shared__ float2 row_ml[MAX_ROWS];  // maximum, 1 / sum
+  __shared__ float2 warp_ml[W];
+  __shared__ float4 warp_o[W][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, M = s.group * s.n_q;
-  const int cta = blockIdx.x;
-  const Split split = work.split[cta];
+  const int worker = blockIdx.x;
+  const Split split = work.split[worker];
+#pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int r = split.row[x];
     if (r < 0) continue;
-    const int c0 = cache::first_cta(split.start[x], split.chunk);
-    const int parts = cache::last_cta(split.start[x], split.n[x], split.chunk) - c0 + 1;
-    auto part = [&](int k) { return cache::part_of(c0 + k, k); };
-    for (int m = warp; m < M; m += JOIN_THREADS / 32) {
-      float top = -INFINITY, z = 0.0f;
-      for (int k = lane; k < parts; k += 32)
-        if (const float2 ml = work.part_ml[(long long)part(k) * M + m]; ml.y != 0.0f) top = fmaxf(top, ml.x);
+    const int w0 = cache::first_worker(split.start[x], split.chunk);
+    const int parts = cache::last_worker(split.start[x], split.pages[x], split.chunk) - w0 + 1;
+    // The row's outputs, four to an element, are shared out among its workers:
+    // `each` elements to a CTA, from element e0 on.
+    const int elements = M * (D / 4), ctas = parts * (int)gridDim.y;
+    const int each = max(2, (elements + ctas - 1) / ctas);
+    const int e0 = min(elements, ((worker - w0) * (int)gridDim.y + (int)blockIdx.y) * each);
+    const int e1 = min(elements, e0 + each);
+    // maximum and sum of the query rows that this CTA needs
+    const int ma = MASS ? 0 : e0 / (D / 4), mb = MASS ? M : (e1 + D / 4 - 1) / (D / 4);
+    auto part = [&](int k, int m) { return (long long)cache::part_of(w0 + k, k == 0) * M + m; };
+    auto put = [&](int m, float2 ml) {
+      const float y = ml.y == 0.0f ? -INFINITY : ml.x + log2f(ml.y);
+      row_lse[x][m] = y;
+      row_ml[m] = make_float2(ml.x, ml.y == 0.0f ? 0.0f : 1.0f / ml.y);
+      if (m * (D / 4) >= e0 && m * (D / 4) < e1) sink.put_lse(a, s, r, m, y);
+    };
+    auto over_warp = [&](float2 ml) {
 #pragma unroll
-      for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, w));
-      const float at = top == -INFINITY ? 0.0f : top;
-      for (int k = lane; k < parts; k += 32) {
-        const float2 ml = work.part_ml[(long long)part(k) * M + m];
-        const float f = ml.y != 0.0f ? tc::ex2(ml.x - at) : 0.0f;
-        factor[k * M + m] = f;
-        z += ml.y * f;
+      for (int o = 16; o > 0; o >>= 1)
+        ml = join_two(ml, make_float2(__shfl_xor_sync(0xFFFFFFFFu, ml.x, o), __shfl_xor_sync(0xFFFFFFFFu, ml.y, o)));
+      return ml;
+    };
+    __syncthreads();  // the row before has been dealt with
+    if (mb - ma >= W || parts <= 32) {
+      for (int m = ma + warp; m < mb; m += W) {
+        float2 ml = make_float2(0.0f, 0.0f);
+        for (int k = lane; k < parts; k += 32) ml = join_two(ml, work.part_ml[part(k, m)]);
+        ml = over_warp(ml);
+        if (lane == 0) put(m, ml);
       }
-#pragma unroll
-      for (int w = 16; w > 0; w >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, w);
-      const float f = z == 0.0f ? 0.0f : 1.0f / z;
-      for (int k = lane; k < parts; k += 32) factor[k * M + m] *= f;
-      if (lane == 0) {
-        const float y = z == 0.0f ? -INFINITY : at + log2f(z);
-        row_lse[x][m] = y;
-        if (cta == c0 && blockIdx.y == 0) sink.put_lse(a, s, r, m, y);
+    } else {
+      for (int m = ma; m < mb; ++m) {
+        float2 ml = make_float2(0.0f, 0.0f);
+        for (int k = tid; k < parts; k += JOIN_THREADS) ml = join_two(ml, work.part_ml[part(k, m)]);
+        ml = over_warp(ml);
+        if (lane == 0) warp_ml[warp] = ml;
+        __syncthreads();
+        if (tid == 0) {
+          for (int w = 1; w < W; ++w) ml = join_two(ml, warp_ml[w]);
+          put(m, ml);
+        }
+        __syncthreads();
       }
     }
     __syncthreads();
-    // the row's outputs, four at a time, shared out among its CTAs
-    const int step = parts * (int)gridDim.y * JOIN_THREADS;
-    for (int e = ((cta - c0) * (int)gridDim.y + (int)blockIdx.y) * JOIN_THREADS + tid; e < M * (D / 4); e += step) {
-      const int m = e / (D / 4), d = e % (D / 4) * 4;
-      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](float4 &o, int e, int k) {
+      const long long at = part(k, e / (D / 4));
+      const float2 ml = work.part_ml[at];
+      const float4 v = *reinterpret_cast<const float4 *>(work.part_o + at * D + e % (D / 4) * 4);
+      const float f = ml.y != 0.0f ? tc::ex2(ml.x - row_ml[e / (D / 4)].x) : 0.0f;
+      o.x += v.x * f;
+      o.y += v.y * f;
+      o.z += v.z * f;
+      o.w += v.w * f;
+    };
+    auto finish = [&](const float4 &o, int e) {
+      const int m = e / (D / 4);
+      const float z = row_ml[m].y;
+      *reinterpret_cast<uint2 *>(sink.o + sink.row(a, s, r, m) * D + e % (D / 4) * 4) =
+          make_uint2(Num<T>::pack(o.x * z, o.y * z), Num<T>::pack(o.z * z, o.w * z));
+    };
+    if (e1 - e0 > 32) {
+      for (int e = e0 + tid; e < e1; e += JOIN_THREADS) {
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-      for (int k = 0; k < parts; ++k) {
-        const float f = factor[k * M + m];
-        const float4 v = *reinterpret_cast<const float4 *>(work.part_o + ((long long)part(k) * M + m) * D + d);
-        o.x += v.x * f;
-        o.y += v.y * f;
-        o.z += v.z * f;
-        o.w += v.w * f;
+        for (int k = 0; k < parts; ++k) add(o, e, k);
+        finish(o, e);
       }
-      *reinterpret_cast<uint2 *>(sink.o + sink.row(a, s, r, m) * D + d) =
-          make_uint2(Num<T>::pack(o.x, o.y), Num<T>::pack(o.z, o.w));
+    } else if (e0 < e1) {
+      // few elements: lanes along them (a power of two), the parts over the
+      // rest of the CTA, summed up by shuffles and through shared memory
+      int wide = 2;
+      while (wide < e1 - e0) wide *= 2;
+      const int e = e0 + lane % wide;
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (e < e1)
+#pragma unroll 4
+        for (int k = tid / wide; k < parts; k += JOIN_THREADS / wide) add(o, e, k);
+      for (int d = wide; d < 32; d *= 2) {
+        o.x += __shfl_xor_sync(0xFFFFFFFFu, o.x, d);
+        o.y += __shfl_xor_sync(0xFFFFFFFFu, o.y, d);
+        o.z += __shfl_xor_sync(0xFFFFFFFFu, o.z, d);
+        o.w += __shfl_xor_sync(0xFFFFFFFFu, o.w, d);
+      }
+      if (lane < wide) warp_o[warp][lane] = o;
+      __syncthreads();
+      if (tid < e1 - e0) {
+        for (int w = 1; w < W; ++w) {
+          const float4 v = warp_o[w][tid];
+          o.x += v.x;
+          o.y += v.y;
+          o.z += v.z;
+          o.w += v.w;
+        }
+        finish(o, e);
+      }
     }
-    __syncthreads();
   }
   if (MASS) {
-    const int u1 = cache::chunk_begin(cta + 1, split.chunk, split.units);
+    __syncthreads();
+    const int rows = a.B * a.H;
+    const int u1 = cache::chunk_begin(worker + 1, split.chunk, split.units);
     const int j = tid % PAGE;
-    for (int u = cache::chunk_begin(cta, split.chunk, split.units) + (int)blockIdx.y * (JOIN_THREADS / PAGE) +
+    for (int u = cache::chunk_begin(worker, split.chunk, split.units) + (int)blockIdx.y * (JOIN_THREADS / PAGE) +
                  tid / PAGE;
          u < u1; u += (int)gridDim.y * (JOIN_THREADS / PAGE)) {
       const int2 at = work.units[u];
-      if (at.y < 0) continue;
+      if (at.x < 0 || at.x >= rows || at.y < 0 || at.y >= a.max_pages) continue;
+      if (at.y * PAGE + j >= a.lens[at.x]) continue;  // behind the last slot
       const float *lse = at.x == split.row[0] ? row_lse[0] : (at.x == split.row[1] ? row_lse[1] : nullptr);
       float got = 0.0f;
       for (int m = 0; m < M; ++m) {

@@ -24,13 +24,14 @@ inline EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// [rows, d] bf16 row-major; box = 64 rows x 64 elements (128 B), 128 B swizzle.
-inline bool make_tile_map(CUtensorMap *map, const void *base, unsigned long long rows, int d) {
+// [rows, d] row-major of 2-byte elements; box = box_rows (64: a tile) rows x
+// 64 elements (128 B), 128 B swizzle.
+inline bool make_tile_map(CUtensorMap *map, const void *base, unsigned long long rows, int d, int box_rows = 64) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)d * 2};
-  cuuint32_t box[2] = {64, 64};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

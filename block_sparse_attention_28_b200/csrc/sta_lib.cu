@@ -426,7 +426,7 @@ sta_status cache_sizes(const sta_kv_cache *c) {
   // rows and rows * max_pages index in 32 bits, the pools' rows are TMA
   // coordinates, sequences go into grid.y
   if (c->B > 65535 || rows >= (1LL << 31) || (long long)c->num_pages * c->kv_heads >= (1LL << 31) / cache::PAGE ||
-      c->max_pages > (1 << 30) / cache::PAGE || rows * c->max_pages >= (1LL << 31))
+      c->max_pages > (1 << 30) / cache::PAGE || rows * (c->max_pages + cache::ROW_COST) >= (1LL << 31))
     return STA_ERR_UNSUPPORTED;
   return STA_OK;
 }
@@ -462,7 +462,7 @@ sta_status decode_sizes(const sta_kv_cache *c, int32_t q_heads, int32_t n_q, int
   return STA_OK;
 }
 
-// Workspace of the attention over a cache: per CTA two parts of rows cut by
+// Workspace of the attention over a cache: per worker two parts of rows cut by
 // its chunk's borders and their description; with accumulation also, per page
 // read, its row and column and its scores, and each row's log-sum-exp.
 struct DecodeWs {
@@ -470,8 +470,9 @@ struct DecodeWs {
 };
 
 DecodeWs decode_ws_layout(const sta_kv_cache *c, int group, int n_q, bool accumulate) {
-  const size_t M = (size_t)group * n_q, parts = 2 * (size_t)decode::MAX_CTAS;
-  const size_t rows = (size_t)c->B * c->kv_heads, units = accumulate ? rows * c->max_pages : 0;
+  const size_t M = (size_t)group * n_q, rows = (size_t)c->B * c->kv_heads;
+  const size_t workers = (size_t)decode::MAX_CTAS * decode::workers_of((int)M), parts = 2 * workers;
+  const size_t units = accumulate ? rows * (c->max_pages + cache::ROW_COST) : 0;
   DecodeWs w;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -481,7 +482,7 @@ DecodeWs decode_ws_layout(const sta_kv_cache *c, int group, int n_q, bool accumu
   };
   w.part_o = take(parts * M * c->d * sizeof(float));
   w.part_ml = take(parts * M * sizeof(float2));
-  w.split = take(decode::MAX_CTAS * sizeof(decode::Split));
+  w.split = take(workers * sizeof(decode::Split));
   w.units = take(units * sizeof(int2));
   w.scores = take(units * M * cache::PAGE * sizeof(float));
   w.lse2 = take(accumulate ? rows * M * sizeof(float) : 0);
@@ -489,7 +490,7 @@ DecodeWs decode_ws_layout(const sta_kv_cache *c, int group, int n_q, bool accumu
   return w;
 }
 
-template <int D, typename T, bool MASS>
+template <int D, int NT, typename T, bool MASS>
 sta_status launch_decode(const sta_kv_cache *c, const cache::Args &a, const decode::Shape &shape, const void *q,
                          void *o, float *lse, uint8_t *ws, cudaStream_t s) {
   using C = decode::Cfg<D>;
@@ -507,13 +508,15 @@ sta_status launch_decode(const sta_kv_cache *c, const cache::Args &a, const deco
   sink.lse = lse;
   CUtensorMap tk, tv;
   const unsigned long long pool_rows = (unsigned long long)c->num_pages * c->kv_heads * cache::PAGE;
-  if (!make_tile_map(&tk, c->k_pages, pool_rows, D) || !make_tile_map(&tv, c->v_pages, pool_rows, D))
+  if (!make_tile_map(&tk, c->k_pages, pool_rows, D, C::KEYS) ||
+      !make_tile_map(&tv, c->v_pages, pool_rows, D, C::KEYS))
     return STA_ERR_CUDA;
-  auto attend = decode::attend_kernel<D, T, MASS>;
+  auto attend = decode::attend_kernel<D, NT, T, MASS>;
   STA_CUDA_TRY(cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
   const long long most = (long long)c->B * c->kv_heads * c->max_pages;
   const int sms = sm_count() < decode::MAX_CTAS ? sm_count() : decode::MAX_CTAS;
   const unsigned ctas = (unsigned)(most < sms ? most : sms);
+  const int workers = decode::workers_of(M);
   attend<<<ctas, decode::THREADS, C::SMEM, s>>>(tk, tv, a, shape, static_cast<const T *>(q), sink, work, wait_limit());
   STA_CUDA_TRY(cudaGetLastError());
   // The join may start up while attend_kernel runs; it waits for its end
@@ -522,9 +525,8 @@ sta_status launch_decode(const sta_kv_cache *c, const cache::Args &a, const deco
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, MASS ? decode::JOIN_SHARES : 1);
+  cfg.gridDim = dim3(ctas * workers, MASS ? decode::JOIN_SHARES : 1);
   cfg.blockDim = dim3(decode::JOIN_THREADS);
-  cfg.dynamicSmemBytes = (size_t)ctas * M * sizeof(float);
   cfg.stream = s;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
@@ -537,8 +539,12 @@ sta_status launch_decode(const sta_kv_cache *c, const cache::Args &a, const deco
 template <int D, typename T>
 sta_status launch_decode_any(const sta_kv_cache *c, const cache::Args &a, const decode::Shape &shape, const void *q,
                              void *o, float *lse, bool accumulate, uint8_t *ws, cudaStream_t s) {
-  return accumulate ? launch_decode<D, T, true>(c, a, shape, q, o, lse, ws, s)
-                    : launch_decode<D, T, false>(c, a, shape, q, o, lse, ws, s);
+  // up to 8 query rows fill one tile of the products, more take two
+  if (shape.group * shape.n_q <= 8)
+    return accumulate ? launch_decode<D, 1, T, true>(c, a, shape, q, o, lse, ws, s)
+                      : launch_decode<D, 1, T, false>(c, a, shape, q, o, lse, ws, s);
+  return accumulate ? launch_decode<D, 2, T, true>(c, a, shape, q, o, lse, ws, s)
+                    : launch_decode<D, 2, T, false>(c, a, shape, q, o, lse, ws, s);
 }
 
 // holes and fills [rows][cap], count [rows]; cap: pairs a row can have

@@ -386,8 +386,9 @@ typedef struct {
                               q, o, k_new, v_new given with this cache */
   int32_t num_pages;       /* pages in k_pages and in v_pages;
                               num_pages * kv_heads * 64 < 2^31 */
-  int32_t max_pages;       /* columns of page_table; B*kv_heads*max_pages < 2^31,
-                              64*max_pages <= 2^30; B <= 65535 */
+  int32_t max_pages;       /* columns of page_table; B <= 65535,
+                              B*kv_heads*(max_pages + 1) < 2^31,
+                              64*max_pages <= 2^30 */
   void *k_pages, *v_pages; /* [num_pages, kv_heads, 64, d], 16-byte aligned */
   const int32_t *page_table; /* [B, max_pages] */
   int32_t *lens;           /* [B, kv_heads] filled slots */

@@ -353,7 +353,7 @@ class KVCache:
             raise ValueError("page_table is [B, max_pages], lens is [B, kv_heads]")
         self.num_pages, self.kv_heads, _, self.d = k_pages.shape
         self.B, self.max_pages = page_table.shape
-        self.dtype, self.device = k_pages.dtype, k_pages.device
+        self.dtype, self.device, self.index = k_pages.dtype, k_pages.device, k_pages.get_device()
         rows, slots = (self.B, self.kv_heads), PAGE * self.max_pages
         self._tensor("k_pages", k_pages, k_pages.dtype, tuple(k_pages.shape))
         self._tensor("v_pages", v_pages, k_pages.dtype, tuple(k_pages.shape))
@@ -367,27 +367,33 @@ class KVCache:
         self.desc = KvCacheDesc(self.B, self.kv_heads, self.d, dtypes[k_pages.dtype], self.num_pages, self.max_pages,
                                 _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(lens), _ptr(seen),
                                 _ptr(slot_pos), _ptr(weight))
+        self._ref = ctypes.byref(self.desc)
 
     def _tensor(self, name, t, dtype, shape, optional=False):
-        """A contiguous tensor of this type and shape on the cache's device."""
+        """A contiguous tensor of this type and shape on the cache's device;
+        its address (None: not given)."""
         if t is None and optional:
-            return
-        if t is None or t.dtype != dtype or t.device != self.device or not t.is_contiguous() or \
-                (shape is not None and tuple(t.shape) != shape):
+            return None
+        if t is None or t.dtype is not dtype or t.get_device() != self.index or not t.is_contiguous() or \
+                (shape is not None and t.shape != shape):
             got = "None" if t is None else f"{t.dtype} {list(t.shape)} strides {list(t.stride())} on {t.device}"
             raise ValueError(f"{name}: contiguous {dtype} {'' if shape is None else list(shape)} on {self.device}, "
                              f"not {got}")
+        return t.data_ptr()
 
-    def _call(self, stream, fn, what):
-        """fn(stream) with the cache's device current; torch's current stream
-        of that device unless one is given."""
-        if self.device.type != "cuda":
+    def _call(self, stream, fn, what, *args):
+        """fn(description, *args, stream) with the cache's device current, on
+        torch's current stream of that device unless one is given."""
+        if self.index < 0:
             raise ValueError(f"{what}: the cache is on {self.device}, not on a GPU")
-        if self.device.index == torch.cuda.current_device():
-            _check(fn(_stream(stream)), what)
-        else:
-            with torch.cuda.device(self.device):
-                _check(fn(_stream(stream)), what)
+        if self.index != torch.cuda.current_device():
+            with torch.cuda.device(self.index):
+                return self._call(stream, fn, what, *args)
+        # (the raw handle: torch.cuda.current_stream() makes an object, 3 us)
+        raw = torch._C._cuda_getCurrentRawStream(self.index) if stream is None else _stream(stream)
+        status = fn(self._ref, *args, raw)
+        if status != STA_OK:
+            raise StaError(status, what)
 
 
 def kv_cache(k_pages, v_pages, page_table, lens, seen=None, slot_pos=None, weight=None):
@@ -401,15 +407,13 @@ def sta_cache_append(cache, k_new, v_new, counts=None, stream=None):
     padded batch that are tokens."""
     n_new = k_new.shape[1] if k_new.dim() == 4 else 0
     shape = (cache.B, n_new, cache.kv_heads, cache.d)
-    cache._tensor("k_new", k_new, cache.dtype, shape)
-    cache._tensor("v_new", v_new, cache.dtype, shape)
-    cache._tensor("counts", counts, torch.int32, (cache.B,), optional=True)
-    cache._call(stream, lambda s: _lib.sta_cache_append(ctypes.byref(cache.desc), _ptr(k_new), _ptr(v_new), n_new,
-                                                        _ptr(counts), s), "sta_cache_append")
+    cache._call(stream, _lib.sta_cache_append, "sta_cache_append",
+                cache._tensor("k_new", k_new, cache.dtype, shape), cache._tensor("v_new", v_new, cache.dtype, shape),
+                n_new, cache._tensor("counts", counts, torch.int32, (cache.B,), True))
 
 
 def sta_attn_fwd_cached_workspace(cache, q_heads, n_q=1, accumulate=False):
-    return int(_lib.sta_attn_fwd_cached_workspace(ctypes.byref(cache.desc), q_heads, n_q, 1 if accumulate else 0))
+    return int(_lib.sta_attn_fwd_cached_workspace(cache._ref, q_heads, n_q, 1 if accumulate else 0))
 
 
 def sta_attn_fwd_cached(cache, q, o, lse, workspace, page_ptr=None, page_idx=None, accumulate=False, sm_scale=0.0,
@@ -418,31 +422,30 @@ def sta_attn_fwd_cached(cache, q, o, lse, workspace, page_ptr=None, page_idx=Non
     over the listed pages of each key head (CSR page_ptr int32
     [B*kv_heads + 1], page_idx int32); accumulate adds each slot's attention
     to cache.weight. workspace: uint8, sta_attn_fwd_cached_workspace() bytes."""
-    n_q, q_heads = (q.shape[1], q.shape[2]) if q.dim() == 4 else (0, 0)
-    cache._tensor("q", q, cache.dtype, (cache.B, n_q, q_heads, cache.d))
-    cache._tensor("o", o, cache.dtype, (cache.B, n_q, q_heads, cache.d))
-    cache._tensor("lse", lse, torch.float32, (cache.B, q_heads, n_q), optional=True)
-    cache._tensor("workspace", workspace, torch.uint8, None)
-    cache._tensor("page_ptr", page_ptr, torch.int32, (cache.B * cache.kv_heads + 1,), optional=True)
-    cache._tensor("page_idx", page_idx, torch.int32, None, optional=True)
+    _, n_q, q_heads, _ = shape = q.shape if q.dim() == 4 else (0, 0, 0, 0)
+    if shape[0] != cache.B or shape[3] != cache.d:
+        raise ValueError(f"q: [{cache.B}, n_q, q_heads, {cache.d}], not {list(q.shape)}")
+    ptr = cache._tensor("page_ptr", page_ptr, torch.int32, (cache.B * cache.kv_heads + 1,), True)
+    idx = cache._tensor("page_idx", page_idx, torch.int32, None, True)
     capacity = 0 if page_idx is None else page_idx.numel()
-    # torch has no address for a tensor of no elements: no list is longer than zero
-    idx = _ptr(page_idx if page_idx is None or capacity else page_ptr)
-    cache._call(stream, lambda s: _lib.sta_attn_fwd_cached(
-        ctypes.byref(cache.desc), _ptr(q), _ptr(o), _ptr(lse), q_heads, n_q, _ptr(page_ptr), idx, capacity,
-        1 if accumulate else 0, _ptr(workspace), workspace.numel(), float(sm_scale), s), "sta_attn_fwd_cached")
+    if capacity == 0 and page_idx is not None:
+        idx = ptr  # torch has no address for a tensor of no elements; none is read
+    cache._call(stream, _lib.sta_attn_fwd_cached, "sta_attn_fwd_cached",
+                cache._tensor("q", q, cache.dtype, shape), cache._tensor("o", o, cache.dtype, shape),
+                cache._tensor("lse", lse, torch.float32, (cache.B, q_heads, n_q), True), q_heads, n_q, ptr, idx,
+                capacity, 1 if accumulate else 0, cache._tensor("workspace", workspace, torch.uint8, None),
+                workspace.numel(), sm_scale)
 
 
 def sta_cache_evict_workspace(cache, budget):
-    return int(_lib.sta_cache_evict_workspace(ctypes.byref(cache.desc), int(budget)))
+    return int(_lib.sta_cache_evict_workspace(cache._ref, budget))
 
 
 def sta_cache_evict(cache, budget, recent, sinks, workspace, stream=None):
     """Cuts every (sequence, head) to `budget` slots: the first `sinks` and the
     `recent` newest positions stay, and the heaviest of the others."""
-    cache._tensor("workspace", workspace, torch.uint8, None)
-    cache._call(stream, lambda s: _lib.sta_cache_evict(ctypes.byref(cache.desc), int(budget), int(recent), int(sinks),
-                                                       _ptr(workspace), workspace.numel(), s), "sta_cache_evict")
+    cache._call(stream, _lib.sta_cache_evict, "sta_cache_evict", budget, recent, sinks,
+                cache._tensor("workspace", workspace, torch.uint8, None), workspace.numel())
 
 
 def sta_set_wait_limit(limit_cycles):

@@ -4,6 +4,8 @@
 // bounds them: a key or value row (128 or 256 B) is read once and written once
 // with 16-byte accesses.
 #pragma once
+#include <cooperative_groups.h>
+
 #include "sta_cache_index.h"
 #include "sta_common.cuh"
 
@@ -95,9 +97,10 @@ append_kernel(Args a, const uint4 *__restrict__ k_new, const uint4 *__restrict__
 }
 
 // -------------------------------------------------------------------- evict
-constexpr int PLAN_THREADS = 1024;
-constexpr int PLAN_WARPS = PLAN_THREADS / 32;
 constexpr int PLAN_BINS = 2048;
+constexpr int PLAN_PASSES = 3;              // 11 + 11 + 10 bits of the key
+constexpr int PLAN_MAX_KEYS = 44 * 1024;    // keys a CTA holds in shared memory
+constexpr int PLAN_UNROLL = 8;
 
 // Order of a slot as an unsigned key: the protected ones above every weight,
 // NaN below every weight, -0 as +0, else the weight's own order.
@@ -119,134 +122,195 @@ __device__ __forceinline__ int warp_scan(int v) {
   return v;
 }
 
-// One CTA per (sequence, head): the budget-th largest key by radix selection
-// (11 + 11 + 10 bits), then, over one contiguous range of slots per warp, the
-// ranks of the ties, of the slots given up below the budget ("holes") and of
-// those kept above it ("fills"). holes and fills [rows, cap], count [rows].
-// Position, weight and length are updated here; the keys and values by
-// move_kernel.
-__global__ void __launch_bounds__(PLAN_THREADS)
-evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int *__restrict__ holes,
+// Slots of a range by what becomes of them: equal to the threshold and below /
+// from the budget on; given up below it; kept from it on.
+struct Tally {
+  int tie_below, tie_above, hole, fill;
+  // Of the range's ties the first `take` stay (slot order: those below the
+  // budget come first): its holes and fills.
+  __device__ __forceinline__ int holes(int take) const { return hole + tie_below - min(take, tie_below); }
+  __device__ __forceinline__ int fills(int take) const { return fill + take - min(take, tie_below); }
+  __device__ __forceinline__ int ties() const { return tie_below + tie_above; }
+};
+
+// A cluster of CTAs per (sequence, head), each with an equal range of the slots
+// and their keys in shared memory (read once; past key_room they are read
+// again). The budget-th largest key is found by radix selection on histograms
+// that every CTA sums up over the cluster; one more pass over the keys counts
+// ties, holes (slots given up below the budget) and fills (slots kept above
+// it) per warp, and a last one lists holes and fills, both in slot order.
+// holes, fills [rows, cap], count [rows]. The length is updated here, the rest
+// by move_kernel. The key reads (8 bytes per slot) are the floor; what bounds
+// it is latency: some ten steps that each wait for the one before.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS)
+evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_room, int *__restrict__ holes,
                   int *__restrict__ fills, int *__restrict__ count) {
-  __shared__ unsigned hist[PLAN_BINS];
-  __shared__ int part[3][PLAN_WARPS];
-  __shared__ unsigned s_prefix;
+  constexpr int W = THREADS / 32;
+  constexpr int PER = PLAN_BINS / THREADS;  // bins of a thread
+  extern __shared__ unsigned plan_smem[];
+  unsigned *hist = plan_smem;                            // [PLAN_PASSES][PLAN_BINS]
+  unsigned *keys = plan_smem + PLAN_PASSES * PLAN_BINS;  // [key_room]
+  __shared__ int part[W];
+  __shared__ Tally tally[W], whole;
+  __shared__ unsigned s_bin;
   __shared__ int s_left;
-  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int r = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int len = a.length(r);
-  if (len <= budget) {
-    if (tid == 0) count[r] = 0;
+  if (len <= budget) {  // for the whole cluster alike
+    if (tid == 0 && rank == 0) count[r] = 0;
     return;
   }
   const int from = a.seen[r] - recent;
-  int *pos = a.pos + a.slot(r, 0);
-  float *weight = a.weight + a.slot(r, 0);
-  auto key_of = [&](int j) { return evict_key(weight[j], pos[j], sinks, from); };
+  const int seg = ((len + ranks - 1) / ranks + 31) / 32 * 32;
+  const int begin = min(len, rank * seg), n = min(len, begin + seg) - begin;
+  const int *pos = a.pos + a.slot(r, begin);
+  const float *weight = a.weight + a.slot(r, begin);
+  auto read_key = [&](int j) { return evict_key(weight[j], pos[j], sinks, from); };
+  auto key_of = [&](int j) { return j < key_room ? keys[j] : read_key(j); };
 
-  unsigned prefix = 0;  // the bits of the threshold found so far
-  int left = budget;    // how many are still to be taken below the bins passed
-  int shift = 32;
-  for (int pass = 0; pass < 3; ++pass) {
-    const int bits = pass < 2 ? 11 : 10;
-    const int next = shift - bits;
-    for (int i = tid; i < PLAN_BINS; i += PLAN_THREADS) hist[i] = 0;
-    __syncthreads();
-    for (int j0 = 0; j0 < len; j0 += PLAN_THREADS) {
-      const int j = j0 + tid;
-      if (j < len) {
-        const unsigned k = key_of(j);
-        if (pass == 0 || (k >> shift) == prefix) atomicAdd(&hist[(k >> next) & ((1u << bits) - 1u)], 1u);
+  for (int i = tid; i < PLAN_PASSES * PLAN_BINS; i += THREADS) hist[i] = 0;
+  __syncthreads();
+  for (int j0 = tid; j0 < n; j0 += THREADS * PLAN_UNROLL) {
+    float w[PLAN_UNROLL];
+    int p[PLAN_UNROLL];
+#pragma unroll
+    for (int x = 0; x < PLAN_UNROLL; ++x) {
+      const int j = j0 + x * THREADS;
+      w[x] = j < n ? weight[j] : 0.0f;
+      p[x] = j < n ? pos[j] : 0;
+    }
+#pragma unroll
+    for (int x = 0; x < PLAN_UNROLL; ++x) {
+      const int j = j0 + x * THREADS;
+      if (j < n) {
+        const unsigned k = evict_key(w[x], p[x], sinks, from);
+        if (j < key_room) keys[j] = k;
+        atomicAdd(&hist[k >> 21], 1u);
       }
     }
+  }
+  unsigned threshold = 0;  // its bits found so far
+  int left = budget;       // keys still to be taken below the bins passed
+  int shift = 21;
+  for (int pass = 0; pass < PLAN_PASSES; ++pass) {
+    const int bits = pass < 2 ? 11 : 10;
+    unsigned *mine = hist + pass * PLAN_BINS;
+    if (pass > 0) {
+      const int next = shift - bits;
+      for (int j = tid; j < n; j += THREADS) {
+        const unsigned k = key_of(j);
+        if ((k >> shift) == threshold) atomicAdd(&mine[(k >> next) & ((1u << bits) - 1u)], 1u);
+      }
+      shift = next;
+    }
+    if (ranks > 1)
+      cluster.sync();
+    else
+      __syncthreads();
+    // the bin, counted from the top, in which the left-th key lies; this
+    // thread's bins are PLAN_BINS - 1 - PER tid and the PER - 1 below
+    int sum[PER], all = 0;
+#pragma unroll
+    for (int x = 0; x < PER; ++x) sum[x] = 0;
+    for (int c = 0; c < ranks; ++c) {
+      const unsigned *theirs = ranks > 1 ? cluster.map_shared_rank(mine, c) : mine;
+#pragma unroll
+      for (int x = 0; x < PER; ++x) sum[x] += (int)theirs[PLAN_BINS - 1 - PER * tid - x];
+    }
+#pragma unroll
+    for (int x = 0; x < PER; ++x) all += sum[x];
+    const int upto = warp_scan(all);
+    if (lane == 31) part[warp] = upto;
     __syncthreads();
-    // the bin, counted from the top, in which the left-th key lies: thread t
-    // holds bins 2047 - 2t and 2046 - 2t
-    const int hi = (int)hist[PLAN_BINS - 1 - 2 * tid], lo = (int)hist[PLAN_BINS - 2 - 2 * tid];
-    const int sum = warp_scan(hi + lo);
-    if (lane == 31) part[0][warp] = sum;
-    __syncthreads();
-    if (warp == 0) part[0][lane] = warp_scan(part[0][lane]);
-    __syncthreads();
-    const int before = (warp > 0 ? part[0][warp - 1] : 0) + sum - hi - lo;
-    if (before < left && left <= before + hi + lo) {
-      const bool top = left <= before + hi;
-      s_prefix = (prefix << bits) | (unsigned)(PLAN_BINS - 1 - 2 * tid - (top ? 0 : 1));
-      s_left = left - before - (top ? 0 : hi);
+    int before = upto - all;
+    for (int w = 0; w < warp; ++w) before += part[w];
+    if (before < left && left <= before + all) {
+      int x = 0;
+#pragma unroll
+      for (int y = 0; y + 1 < PER; ++y)
+        if (x == y && left > before + sum[y]) {
+          before += sum[y];
+          ++x;
+        }
+      s_bin = (unsigned)(PLAN_BINS - 1 - PER * tid - x);
+      s_left = left - before;
     }
     __syncthreads();
-    prefix = s_prefix;
+    threshold = (threshold << bits) | s_bin;
     left = s_left;
-    shift = next;
-    __syncthreads();
   }
   // keep: above the threshold, and the first `left` of its equals
-  const unsigned threshold = prefix;
-  const int seg = (len + PLAN_THREADS - 1) / PLAN_THREADS * 32;
-  const int lo = min(len, warp * seg), hi = min(len, lo + seg);
-  const unsigned below_lane = (1u << lane) - 1u;
-  int ties = 0;
-  for (int j0 = lo; j0 < hi; j0 += 32)
-    ties += __popc(__ballot_sync(0xFFFFFFFFu, j0 + lane < hi && key_of(j0 + lane) == threshold));
-  if (lane == 0) part[0][warp] = ties;
+  const int each = ((n + W - 1) / W + 31) / 32 * 32;  // a warp's slots
+  const int lo = min(n, warp * each), hi = min(n, lo + each);
+  const int edge = budget - begin;  // first local slot past the budget
+  Tally mine = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int j = lo + lane; j < hi; j += 32) {
+    const unsigned k = key_of(j);
+    const bool below = j < edge;
+    mine.tie_below += k == threshold && below;
+    mine.tie_above += k == threshold && !below;
+    mine.hole += k < threshold && below;
+    mine.fill += k > threshold && !below;
+  }
+  mine.tie_below = __reduce_add_sync(0xFFFFFFFFu, mine.tie_below);
+  mine.tie_above = __reduce_add_sync(0xFFFFFFFFu, mine.tie_above);
+  mine.hole = __reduce_add_sync(0xFFFFFFFFu, mine.hole);
+  mine.fill = __reduce_add_sync(0xFFFFFFFFu, mine.fill);
+  if (lane == 0) tally[warp] = mine;
   __syncthreads();
   if (warp == 0) {
-    const int v = part[0][lane];
-    part[0][lane] = warp_scan(v) - v;
+    Tally v = {0, 0, 0, 0};
+    if (lane < W) v = tally[lane];
+    v.tie_below = __reduce_add_sync(0xFFFFFFFFu, v.tie_below);
+    v.tie_above = __reduce_add_sync(0xFFFFFFFFu, v.tie_above);
+    v.hole = __reduce_add_sync(0xFFFFFFFFu, v.hole);
+    v.fill = __reduce_add_sync(0xFFFFFFFFu, v.fill);
+    if (lane == 0) whole = v;
   }
-  __syncthreads();
-  // twice over the range: count the holes and fills of the range, then list them
-  int n_holes = 0, n_fills = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int tie = part[0][warp];
-    int hole = pass ? part[1][warp] : 0, fill = pass ? part[2][warp] : 0;
-    for (int j0 = lo; j0 < hi; j0 += 32) {
-      const int j = j0 + lane;
-      const bool in = j < hi;
-      const unsigned k = in ? key_of(j) : 0u;
-      const bool equal = in && k == threshold;
-      const unsigned eq = __ballot_sync(0xFFFFFFFFu, equal);
-      const bool keep = in && (k > threshold || (equal && tie + __popc(eq & below_lane) < left));
-      const unsigned hm = __ballot_sync(0xFFFFFFFFu, in && !keep && j < budget);
-      const unsigned fm = __ballot_sync(0xFFFFFFFFu, keep && j >= budget);
-      if (pass) {
-        const int at_hole = hole + __popc(hm & below_lane), at_fill = fill + __popc(fm & below_lane);
-        if ((hm >> lane & 1u) && at_hole < cap) holes[(long long)r * cap + at_hole] = j;
-        if ((fm >> lane & 1u) && at_fill < cap) fills[(long long)r * cap + at_fill] = j;
-      }
-      tie += __popc(eq);
-      hole += __popc(hm);
-      fill += __popc(fm);
-    }
-    if (!pass) {
-      if (lane == 0) {
-        part[1][warp] = hole;
-        part[2][warp] = fill;
-      }
-      __syncthreads();
-      if (warp < 2) {
-        const int v = part[1 + warp][lane];
-        const int s = warp_scan(v);
-        part[1 + warp][lane] = s - v;
-        if (lane == 31) hist[warp] = (unsigned)s;
-      }
-      __syncthreads();
-      n_holes = (int)hist[0];
-      n_fills = (int)hist[1];
-    }
+  if (ranks > 1)
+    cluster.sync();
+  else
+    __syncthreads();
+  // ties, holes and fills before this warp's range
+  int tie = 0, hole = 0, fill = 0;
+  auto pass_over = [&](const Tally &v) {
+    const int take = max(0, min(left - tie, v.ties()));
+    hole += v.holes(take);
+    fill += v.fills(take);
+    tie += v.ties();
+  };
+  for (int c = 0; c < rank; ++c) pass_over(*cluster.map_shared_rank(&whole, c));
+  for (int w = 0; w < warp; ++w) pass_over(tally[w]);
+  const unsigned below_lane = (1u << lane) - 1u;
+  for (int j0 = lo; j0 < hi; j0 += 32) {
+    const int j = j0 + lane;
+    const bool in = j < hi;
+    const unsigned k = in ? key_of(j) : 0u;
+    const bool equal = in && k == threshold;
+    const unsigned eq = __ballot_sync(0xFFFFFFFFu, equal);
+    const bool keep = in && (k > threshold || (equal && tie + __popc(eq & below_lane) < left));
+    const unsigned hm = __ballot_sync(0xFFFFFFFFu, in && !keep && j < edge);
+    const unsigned fm = __ballot_sync(0xFFFFFFFFu, keep && j >= edge);
+    const int at_hole = hole + __popc(hm & below_lane), at_fill = fill + __popc(fm & below_lane);
+    if ((hm >> lane & 1u) && at_hole < cap) holes[(long long)r * cap + at_hole] = begin + j;
+    if ((fm >> lane & 1u) && at_fill < cap) fills[(long long)r * cap + at_fill] = begin + j;
+    tie += __popc(eq);
+    hole += __popc(hm);
+    fill += __popc(fm);
   }
-  __syncthreads();
-  // as many holes as fills: `budget` slots stay in all (and never more than
-  // the lists hold)
-  const int n = min(min(n_holes, n_fills), cap);
-  for (int i = tid; i < n; i += PLAN_THREADS) {
-    const int to = holes[(long long)r * cap + i], of = fills[(long long)r * cap + i];
-    pos[to] = pos[of];
-    weight[to] = weight[of];
-  }
-  if (tid == 0) {
-    count[r] = n;
+  if (rank == ranks - 1 && warp == W - 1 && lane == 0) {
+    // as many holes as fills: `budget` slots stay in all (and never more than
+    // the lists hold)
+    count[r] = min(min(hole, fill), cap);
     a.lens[r] = budget;
   }
+  if (ranks > 1) cluster.sync();  // the others have read this CTA's memory
 }
 
 constexpr int MOVE_THREADS = 256;
@@ -258,16 +322,17 @@ __host__ __device__ constexpr int move_pairs() {
 }
 
 // grid.x = row, grid.y strides over its pairs; D/8 threads move one pair's key
-// and value, MOVE_UNROLL pairs in flight each.
+// and value, MOVE_UNROLL pairs in flight each, the first of them the position
+// and the weight. Sources and destinations are disjoint.
 template <int D>
 __global__ void __launch_bounds__(MOVE_THREADS)
-move_kernel(Args a, int cap, const int *__restrict__ holes, const int *__restrict__ fills,
-            const int *__restrict__ count) {
+move_kernel(Args a, int cap, const int *holes, const int *fills, const int *count) {
   constexpr int CPR = D / 8;
   constexpr int GROUPS = MOVE_THREADS / CPR;
   const int r = blockIdx.x, b = r / a.H, h = r - b * a.H;
-  const int n = count[r];
   const int chunk = threadIdx.x % CPR, group = threadIdx.x / CPR;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int n = count[r];
   for (int i0 = (int)blockIdx.y * move_pairs<D>(); i0 < n; i0 += (int)gridDim.y * move_pairs<D>()) {
     uint4 k[MOVE_UNROLL], v[MOVE_UNROLL];
     long long dst[MOVE_UNROLL];
@@ -283,6 +348,10 @@ move_kernel(Args a, int cap, const int *__restrict__ holes, const int *__restric
           dst[u] = a.row(pt, h, to) * CPR + chunk;
           k[u] = a.k[src];
           v[u] = a.v[src];
+        }
+        if (chunk == 0) {
+          a.pos[a.slot(r, to)] = a.pos[a.slot(r, of)];
+          a.weight[a.slot(r, to)] = a.weight[a.slot(r, of)];
         }
       }
     }

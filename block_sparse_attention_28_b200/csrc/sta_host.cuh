@@ -2,6 +2,8 @@
 // tensor-map encoding through the runtime's driver entry point (no -lcuda),
 // the SM count and the device check.
 #pragma once
+#include <atomic>
+
 #include "sta_common.cuh"
 
 namespace sta {
@@ -51,6 +53,21 @@ inline bool device_is_sm100() {
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return false;
   if (cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) return false;
   return major == 10 && minor == 0;
+}
+
+// SMs of the current device if it is a B200 (sm_100), else 0; asked once per
+// device.
+inline int sm100_count() {
+  constexpr int MAX_DEVICES = 64;
+  static std::atomic<int> known[MAX_DEVICES];  // SMs + 1, or 1: another GPU
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return 0;
+  int v = known[dev].load(std::memory_order_relaxed);
+  if (v == 0) {
+    v = 1 + (device_is_sm100() ? sm_count() : 0);
+    known[dev].store(v, std::memory_order_relaxed);
+  }
+  return v - 1;
 }
 
 }  // namespace sta

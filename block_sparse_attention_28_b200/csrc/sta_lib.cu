@@ -514,7 +514,7 @@ sta_status launch_decode(const sta_kv_cache *c, const cache::Args &a, const deco
   auto attend = decode::attend_kernel<D, NT, T, MASS>;
   STA_CUDA_TRY(cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
   const long long most = (long long)c->B * c->kv_heads * c->max_pages;
-  const int sms = sm_count() < decode::MAX_CTAS ? sm_count() : decode::MAX_CTAS;
+  const int sms = sm100_count() < decode::MAX_CTAS ? sm100_count() : decode::MAX_CTAS;
   const unsigned ctas = (unsigned)(most < sms ? most : sms);
   const int workers = decode::workers_of(M);
   attend<<<ctas, decode::THREADS, C::SMEM, s>>>(tk, tv, a, shape, static_cast<const T *>(q), sink, work, wait_limit());
@@ -564,6 +564,56 @@ EvictWs evict_ws_layout(const sta_kv_cache *c, int32_t budget) {
   w.count = w.fills + align_up(rows * w.cap * sizeof(int), 256);
   w.total = w.count + align_up(rows * sizeof(int), 256);
   return w;
+}
+
+// One CTA per row, or a cluster of up to 8 for long rows: as long as a CTA has
+// more than 8192 slots and the GPU (two of the large CTAs per SM) has room, or
+// the keys do not fit in its shared memory.
+template <int THREADS>
+sta_status launch_plan(const sta_kv_cache *c, const cache::Args &a, int budget, int recent, int sinks, int cap,
+                       int *holes, int *fills, int *count, cudaStream_t s) {
+  const long long rows = (long long)c->B * c->kv_heads, slots = (long long)cache::PAGE * c->max_pages;
+  int ranks = 1;
+  while (ranks < 8 && slots / ranks > 8192 &&
+         (rows * ranks * 2 <= 2 * decode::MAX_CTAS || slots / ranks > cache::PLAN_MAX_KEYS))
+    ranks *= 2;
+  if (rows * ranks >= (1LL << 31)) return STA_ERR_UNSUPPORTED;
+  const long long share = (slots / ranks + 63) / 32 * 32;
+  const int room = (int)(share < cache::PLAN_MAX_KEYS ? share : cache::PLAN_MAX_KEYS);
+  const size_t smem = ((size_t)cache::PLAN_PASSES * cache::PLAN_BINS + room) * sizeof(unsigned);
+  STA_CUDA_TRY(cudaFuncSetAttribute(cache::evict_plan_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)smem));
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = (unsigned)ranks;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * ranks));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = 1;
+  STA_CUDA_TRY(cudaLaunchKernelEx(&cfg, cache::evict_plan_kernel<THREADS>, a, budget, recent, sinks, cap, room, holes,
+                                  fills, count));
+  return STA_OK;
+}
+
+template <int D>
+sta_status launch_move(const sta_kv_cache *c, const cache::Args &a, int cap, const int *holes, const int *fills,
+                       const int *count, cudaStream_t s) {
+  const long long passes = ((long long)cap + cache::move_pairs<D>() - 1) / cache::move_pairs<D>();
+  cudaLaunchAttribute early;  // starts up while the plan is made, waits for its end
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(c->B * c->kv_heads), (unsigned)(passes < 65535 ? passes : 65535));
+  cfg.blockDim = dim3(cache::MOVE_THREADS);
+  cfg.stream = s;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  STA_CUDA_TRY(cudaLaunchKernelEx(&cfg, cache::move_kernel<D>, a, cap, holes, fills, count));
+  return STA_OK;
 }
 
 }  // namespace
@@ -832,7 +882,7 @@ sta_status sta_cache_append(const sta_kv_cache *cache, const void *k_new, const 
       n_new < 1)
     return STA_ERR_INVALID_ARG;
   if ((long long)n_new * cache->kv_heads * cache->d >= (1LL << 31)) return STA_ERR_UNSUPPORTED;
-  if (!device_is_sm100()) return STA_ERR_UNSUPPORTED;
+  if (sm100_count() == 0) return STA_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const long long chunks = (long long)n_new * cache->kv_heads * (cache->d / 8);
   const long long per_cta = cache::APPEND_THREADS * cache::APPEND_UNROLL;
@@ -872,7 +922,7 @@ sta_status sta_attn_fwd_cached(const sta_kv_cache *cache, const void *q, void *o
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
       ws_bytes < decode_ws_layout(cache, group, n_q, accumulate != 0).total)
     return STA_ERR_WORKSPACE;
-  if (!device_is_sm100()) return STA_ERR_UNSUPPORTED;
+  if (sm100_count() == 0) return STA_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   decode::Shape shape;
   shape.group = group;
@@ -905,25 +955,18 @@ sta_status sta_cache_evict(const sta_kv_cache *cache, int32_t budget, int32_t re
   const EvictWs w = evict_ws_layout(cache, budget);
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || ws_bytes < w.total)
     return STA_ERR_WORKSPACE;
-  if (!device_is_sm100()) return STA_ERR_UNSUPPORTED;
+  if (sm100_count() == 0) return STA_ERR_UNSUPPORTED;
   if (w.cap == 0) return STA_OK;  // the page table holds no more than the budget
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   int *holes = reinterpret_cast<int *>(ws + w.holes), *fills = reinterpret_cast<int *>(ws + w.fills);
   int *count = reinterpret_cast<int *>(ws + w.count);
-  const unsigned rows = (unsigned)(cache->B * cache->kv_heads);
-  cache::evict_plan_kernel<<<rows, cache::PLAN_THREADS, 0, s>>>(a, budget, recent, sinks, w.cap, holes, fills,
-                                                                count);
-  STA_CUDA_TRY(cudaGetLastError());
-  const int pairs = cache->d == 128 ? cache::move_pairs<128>() : cache::move_pairs<64>();
-  const long long passes = ((long long)w.cap + pairs - 1) / pairs;
-  const dim3 grid(rows, (unsigned)(passes < 65535 ? passes : 65535));
-  if (cache->d == 128)
-    cache::move_kernel<128><<<grid, cache::MOVE_THREADS, 0, s>>>(a, w.cap, holes, fills, count);
-  else
-    cache::move_kernel<64><<<grid, cache::MOVE_THREADS, 0, s>>>(a, w.cap, holes, fills, count);
-  STA_CUDA_TRY(cudaGetLastError());
-  return STA_OK;
+  sta_status run = cache::PAGE * cache->max_pages <= 4096
+                       ? launch_plan<256>(cache, a, budget, recent, sinks, w.cap, holes, fills, count, s)
+                       : launch_plan<1024>(cache, a, budget, recent, sinks, w.cap, holes, fills, count, s);
+  if (run != STA_OK) return run;
+  return cache->d == 128 ? launch_move<128>(cache, a, w.cap, holes, fills, count, s)
+                         : launch_move<64>(cache, a, w.cap, holes, fills, count, s);
 }
 
 sta_status sta_set_wait_limit(int64_t limit_cycles) {

@@ -426,6 +426,58 @@ def test_evict_equal_weights_go_by_slot(sta):
     C.same_as(t, c)
 
 
+@pytest.mark.parametrize("lens,kv,budget,recent,sinks,ties", [
+    ([20_000, 17_000, 300], 2, 5000, 700, 9, False),   # clusters of 2 CTAs, of 4 and of 8
+    ([40_001], 1, 39_999, 5, 0, True),
+    ([100_003, 64], 1, 20_000, 9000, 64, False),
+    ([90_000], 3, 30_000, 0, 0, True),
+    ([70_000], 200, 100, 10, 2, True),                # many rows: two CTAs, for the keys' sake
+])
+def test_evict_long_rows(sta, lens, kv, budget, recent, sinks, ties):
+    """Rows shared out over a cluster of CTAs, with few equal weights and with
+    hardly any others."""
+    d, B = 64, len(lens)
+    need = [-(-n // C.PAGE) for n in lens]
+    num, width = sum(need), max(need)
+    g = torch.Generator(device="cuda").manual_seed(budget)
+    t = {n: torch.randint(-30000, 30000, (num, kv, C.PAGE, d), generator=g, device="cuda",
+                          dtype=torch.int16).view(torch.bfloat16) for n in ("k_pages", "v_pages")}
+    order = torch.randperm(num, generator=g, device="cuda").int()
+    table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+    for b in range(B):
+        table[b, :need[b]] = order[sum(need[:b]):sum(need[:b + 1])]
+    length = torch.tensor(lens, dtype=torch.int32, device="cuda")[:, None].expand(B, kv).contiguous()
+    w = torch.rand(B, kv, C.PAGE * width, generator=g, device="cuda")
+    t.update(page_table=table, lens=length, seen=length.clone(), weight=(w * 3).floor() if ties else w,
+             slot_pos=torch.rand(w.shape, generator=g, device="cuda").argsort(-1).int())
+    want = {n: x.clone() for n, x in t.items()}
+    evict(sta, t, budget, recent, sinks)
+    ok(sta)
+    for b in range(B):
+        n = lens[b]
+        if n <= budget:
+            continue
+        for h in range(kv):
+            p, x = want["slot_pos"][b, h, :n], want["weight"][b, h, :n].double()
+            safe = (p < sinks) | (p >= n - recent)
+            key = torch.where(safe, 1e9, x)
+            stay = torch.zeros(n, dtype=torch.bool, device="cuda")
+            stay[torch.sort(key, descending=True, stable=True).indices[:budget]] = True
+            to = (~stay[:budget]).nonzero()[:, 0]
+            of = budget + stay[budget:].nonzero()[:, 0]
+            for name in ("k_pages", "v_pages"):
+                pool = want[name].view(torch.int16)
+                pool[table[b, to // C.PAGE].long(), h, to % C.PAGE] = \
+                    pool[table[b, of // C.PAGE].long(), h, of % C.PAGE]
+            for name in ("slot_pos", "weight"):
+                want[name][b, h, to] = want[name][b, h, of]
+            want["lens"][b, h] = budget
+    for name in ("k_pages", "v_pages"):
+        assert torch.equal(t[name].view(torch.int16), want[name].view(torch.int16)), name
+    for name in ("slot_pos", "weight", "lens", "seen"):
+        assert torch.equal(t[name], want[name]), name
+
+
 def test_evict_special_weights(sta):
     """Infinite, NaN, negative, subnormal weights; what is protected stays
     whatever its weight."""

@@ -19,10 +19,10 @@
 // the running maximum and sum and the outputs of its query rows in registers;
 // rows cut by a chunk border leave their parts (the sum relative to a maximum)
 // in the workspace.
-// join_kernel: joins those parts, and adds every slot's attention to its
-// weight once the row's log-sum-exp is known, from the scores that
-// attend_kernel left (4 bytes per slot and query row against 4 d for its key
-// and value).
+// join_kernel: joins those parts.
+// weigh_kernel: adds every slot's attention to its weight now that the rows'
+// log-sum-exps are known, from the scores that attend_kernel left (4 bytes per
+// slot and query row against 4 d for its key and value).
 #pragma once
 #include <cuda_fp16.h>
 
@@ -36,24 +36,28 @@ using cache::Args;
 using cache::PAGE;
 
 constexpr int MAX_CTAS = 148;  // one per SM of a B200
-constexpr int WARPS = 8;
-constexpr int THREADS = 32 * WARPS;
+constexpr int MAX_WARPS = 8;
 constexpr int MAX_ROWS = 64;  // query rows per key head
-constexpr int STAGE_BYTES = 8192;
-constexpr int RING_BYTES = 24 * STAGE_BYTES;  // of all workers
+constexpr int KEYS = 32;      // slots of a stage of the ring
+constexpr int KT = KEYS / 16;
+constexpr int HALF_BYTES = KEYS * 128;  // 64 values of every slot
+constexpr int MAX_STAGES = 28;          // of all workers
 constexpr long long DRAIN_LIMIT = 200000000LL;
 
-// Warps of a worker (16 query rows each) and workers of a CTA.
+// Warps of a worker (16 query rows each) and workers of a CTA. Seven workers
+// of one warp have two stages of 16 KB each at d = 128, which is what shared
+// memory holds.
 __host__ __device__ inline int tiles_of(int M) { return M <= 16 ? 1 : (M <= 32 ? 2 : 4); }
-__host__ __device__ inline int workers_of(int M) { return WARPS / tiles_of(M); }
+__host__ __device__ inline int workers_of(int M) { return M <= 16 ? 7 : (M <= 32 ? 4 : 2); }
+__host__ __device__ inline int warps_of(int M) { return tiles_of(M) * workers_of(M); }
 
 template <int D>
 struct Cfg {
-  static constexpr int KEYS = STAGE_BYTES / (4 * D);        // slots of a stage: 16 or 32
-  static constexpr int KT = KEYS / 16;
-  static constexpr int HALF_BYTES = KEYS * 128;             // 64 values of every slot
   static constexpr int TILE_BYTES = HALF_BYTES * (D / 64);  // keys or values of a stage
-  static constexpr int SMEM = 1024 + RING_BYTES;
+  static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+  // stages of a worker: 2, 3, 6 at d = 128, twice as many at d = 64
+  static __host__ __device__ inline int stages(int M) { return (M <= 16 ? 2 : (M <= 32 ? 3 : 6)) * (128 / D); }
+  static int smem(int M) { return 1024 + workers_of(M) * stages(M) * STAGE_BYTES; }
 };
 
 struct Shape {
@@ -75,10 +79,14 @@ struct Work {
   float *part_o;      // [2 * workers][M][D]
   float2 *part_ml;    // [2 * workers][M] maximum (log2) and sum
   Split *split;       // [workers]
-  int2 *units;        // [units] (row, column of the page table) of a page, else -1
+  // for weigh_kernel (else NULL)
+  int2 *units;        // [units] row, and packed column and filled slots, of a page; else -1
   float *scores;      // [units][M][PAGE] s_j log2 e, -inf out of view
-  float *lse2;        // [rows][M] log-sum-exp (log2) of the rows held whole
+  float *lse2;        // [rows][M] log-sum-exp (log2)
 };
+
+// A page's column (below 2^24) and its filled slots (1 to PAGE).
+__device__ __forceinline__ int pack_page(int col, int held) { return col | (min(held, PAGE) - 1) << 24; }
 
 // What a worker's warps are told of a stage.
 enum : int { FIRST = 1, LAST = 2, WHOLE = 4, BEGINS = 8, SKIP = 16, END = 32, SUB_SHIFT = 8 };
@@ -244,7 +252,8 @@ struct Producer {
         split->pages[begins] = n;
       }
     }
-    if (units != nullptr && lane < take) units[w_unit] = page_unit ? make_int2(w_row, col) : make_int2(-1, -1);
+    if (units != nullptr && lane < take)
+      units[w_unit] = col >= 0 ? make_int2(w_row, pack_page(col, w_held)) : make_int2(-1, -1);
     left = __ballot_sync(0xFFFFFFFFu, page_unit);
     sub = 0;
     if (take > 0) {  // the unit after the batch
@@ -269,23 +278,23 @@ struct Producer {
     const int x = none ? 0 : __ffs(left) - 1;
     int state = 0;
     if (lane == x) {
-      const bool last = none || (w_flags & SKIP) || w_held <= (sub + 1) * C::KEYS || (sub + 1) * C::KEYS == PAGE;
+      const bool last = none || (w_flags & SKIP) || w_held <= (sub + 1) * KEYS || (sub + 1) * KEYS == PAGE;
       int flags = none ? (SKIP | END) : w_flags | sub << SUB_SHIFT;
       if (sub > 0) flags &= ~FIRST;
       if (!last) flags &= ~(LAST | END);
       if (issued < stages || tc::mbar_wait(&empty[stage], ((issued / stages) & 1) ^ 1, abort, limit)) {
-        piece[stage] = Piece{w_row, w_unit, w_held - sub * C::KEYS, flags};
+        piece[stage] = Piece{w_row, w_unit, w_held - sub * KEYS, flags};
         if (flags & SKIP) {
           tc::mbar_arrive(&full[stage]);
         } else {
-          const uint32_t dst = tc::smem_u32(ring + stage * STAGE_BYTES);
-          const int y = w_y + sub * C::KEYS;
-          tc::mbar_expect_tx(&full[stage], STAGE_BYTES);
+          const uint32_t dst = tc::smem_u32(ring + stage * C::STAGE_BYTES);
+          const int y = w_y + sub * KEYS;
+          tc::mbar_expect_tx(&full[stage], C::STAGE_BYTES);
 #pragma unroll
-          for (int e = 0; e < D / 64; ++e) tc::tma_load_2d(dst + e * C::HALF_BYTES, &tk, &full[stage], 64 * e, y);
+          for (int e = 0; e < D / 64; ++e) tc::tma_load_2d(dst + e * HALF_BYTES, &tk, &full[stage], 64 * e, y);
 #pragma unroll
           for (int e = 0; e < D / 64; ++e)
-            tc::tma_load_2d(dst + C::TILE_BYTES + e * C::HALF_BYTES, &tv, &full[stage], 64 * e, y);
+            tc::tma_load_2d(dst + C::TILE_BYTES + e * HALF_BYTES, &tv, &full[stage], 64 * e, y);
         }
         state = 1 | (last ? 2 : 0) | (flags & END);
       }
@@ -343,52 +352,58 @@ __device__ __forceinline__ void load_queries(const T *q, const Args &a, const Sh
   }
 }
 
-// One stage (its keys at kt, its values at vt): scores, softmax step, weighted
-// values. lim[n][y]: how many of its slots query row 8 n + 2 t + y sees; held:
-// how many are filled (either may be negative or above KEYS). edge: any of
-// these is below KEYS. scores: where query row 0's scores go (MASS), of which
-// the warp has `rows` rows.
-template <int D, int NT, typename T, bool MASS>
-__device__ __forceinline__ void attend_slots(uint32_t kt, uint32_t vt, const uint32_t (&qb)[NT][D / 16][2],
-                                             const Shape &s, const int (&lim)[NT][2], int held, bool edge,
-                                             Tile<D, NT> &acc, float *scores, int rows) {
-  using N = Num<T>;
-  using C = Cfg<D>;
-  constexpr int KT = C::KT;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  // ldmatrix addresses: lane -> (row lane % 8 of matrix lane / 8)
-  const int l7 = lane & 7, m8 = lane >> 3;
-  float p[KT][NT][4];
-  {
-    // A = K: matrices (slots 0..7, 8..15) x (16-byte pieces 2 ks, 2 ks + 1).
-    // Two chains of additions each for the even and the odd steps.
-    float odd_p[KT][NT][4];
-    const uint32_t row = kt + (l7 + (m8 & 1) * 8) * 128;
+// Where a lane's ldmatrix rows lie in a stage (128-byte swizzle: 16-byte piece c
+// of slot j is at piece c ^ (j % 8) of its 128 bytes), for pieces 2 j, 2 j + 1.
+struct Lanes {
+  uint32_t k[4], v[4];
+  template <int D>
+  __device__ __forceinline__ void init() {
+    const int lane = threadIdx.x & 31, l7 = lane & 7, m8 = lane >> 3;  // row l7 of matrix m8
 #pragma unroll
-    for (int x = 0; x < KT; ++x)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) p[x][n][e] = odd_p[x][n][e] = 0.0f;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-      for (int x = 0; x < KT; ++x) {
-        uint32_t ka[4];
-        ldmatrix(row + x * 2048 + (ks >> 2) * C::HALF_BYTES + ((((ks & 3) * 2 + (m8 >> 1)) ^ l7) << 4), ka);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) N::mma(ks & 1 ? odd_p[x][n] : p[x][n], ka, qb[n][ks][0], qb[n][ks][1]);
-      }
-#pragma unroll
-    for (int x = 0; x < KT; ++x)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[x][n][e] = (p[x][n][e] + odd_p[x][n][e]) * s.scale_log2;
-          if (edge && 16 * x + g + 8 * (e >> 1) >= lim[n][e & 1]) p[x][n][e] = -INFINITY;
-        }
+    for (int j = 0; j < 4; ++j) {
+      // A = K: matrices (slots 0..7, 8..15) x (pieces 2 j, 2 j + 1)
+      k[j] = (l7 + (m8 & 1) * 8) * 128 + (((m8 >> 1) ^ l7 ^ (2 * j)) << 4);
+      // A = V^T: matrices (pieces 2 j, 2 j + 1) x (slots 0..7, 8..15)
+      v[j] = Cfg<D>::TILE_BYTES + (l7 + (m8 >> 1) * 8) * 128 + (((m8 & 1) ^ l7 ^ (2 * j)) << 4);
+    }
   }
+};
+
+// One stage: scores, softmax step, weighted values. lim[n][y]: how many of its
+// slots query row 8 n + 2 t + y sees; held: how many are filled (either may be
+// negative or above KEYS). EDGE: any of these is below KEYS. scores: where
+// query row 0's scores go (MASS), of which the warp has `rows` rows.
+template <int D, int NT, typename T, bool MASS, bool EDGE>
+__device__ __forceinline__ void attend_slots(uint32_t stage, const Lanes &lanes, const uint32_t (&qb)[NT][D / 16][2],
+                                             const Shape &s, const int (&lim)[NT][2], int held, Tile<D, NT> &acc,
+                                             float *scores, int rows) {
+  using N = Num<T>;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  float p[KT][NT][4];
+#pragma unroll
+  for (int x = 0; x < KT; ++x)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[x][n][e] = 0.0f;
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+    for (int x = 0; x < KT; ++x) {
+      uint32_t ka[4];
+      ldmatrix(stage + lanes.k[ks & 3] + x * 2048 + (ks >> 2) * HALF_BYTES, ka);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) N::mma(p[x][n], ka, qb[n][ks][0], qb[n][ks][1]);
+    }
+#pragma unroll
+  for (int x = 0; x < KT; ++x)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        p[x][n][e] = __fmul_rn(p[x][n][e], s.scale_log2);  // the score that is kept, with or without MASS
+        if (EDGE && 16 * x + g + 8 * (e >> 1) >= lim[n][e & 1]) p[x][n][e] = -INFINITY;
+      }
   if (MASS) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -436,7 +451,6 @@ __device__ __forceinline__ void attend_slots(uint32_t kt, uint32_t vt, const uin
   // weight of 0 (0 * inf): those of slots >= held are cleared. A slot that only
   // the newer of the n_q tokens see is cleared where it is not finite, and what
   // is not finite added by hand for those who see it.
-  auto slots_below = [&](int key) { return key + 1 < held ? 0xFFFFFFFFu : (key < held ? 0xFFFFu : 0u); };
   auto finite = [](uint32_t v) {
     return ((v & N::NONFINITE) == N::NONFINITE ? 0u : v & 0xFFFFu) |
            ((v >> 16 & N::NONFINITE) == N::NONFINITE ? 0u : v & 0xFFFF0000u);
@@ -445,12 +459,13 @@ __device__ __forceinline__ void attend_slots(uint32_t kt, uint32_t vt, const uin
     uint32_t v;
     asm volatile("ld.shared.u16 %0, [%1];"
                  : "=r"(v)
-                 : "r"(vt + (d >> 6) * C::HALF_BYTES + key * 128 + ((((d & 63) >> 3) ^ (key & 7)) << 4) + (d & 7) * 2));
+                 : "r"(stage + Cfg<D>::TILE_BYTES + (d >> 6) * HALF_BYTES + key * 128 +
+                       ((((d & 63) >> 3) ^ (key & 7)) << 4) + (d & 7) * 2));
     return v;
   };
   bool odd = false;
-  if (edge && s.n_q > 1) {
-    for (int key = max(0, held - (s.n_q - 1)); key < min(C::KEYS, held); ++key)
+  if (EDGE && s.n_q > 1) {
+    for (int key = max(0, held - (s.n_q - 1)); key < min(KEYS, held); ++key)
       for (int d = lane; d < D; d += 32) odd |= (value(key, d) & N::NONFINITE) == N::NONFINITE;
     odd = __any_sync(0xFFFFFFFFu, odd);
   }
@@ -469,14 +484,17 @@ __device__ __forceinline__ void attend_slots(uint32_t kt, uint32_t vt, const uin
         hi[n][e] = transpose(v);
         lo[n][e] = transpose(N::pack(p0 - r.x, p1 - r.y));
       }
-    // A = V^T: matrices (16-byte pieces 2 c, 2 c + 1) x (slots 0..7, 8..15)
-    const uint32_t row = vt + (x * 16 + l7 + (m8 >> 1) * 8) * 128;
-    const uint32_t m0 = slots_below(16 * x + 2 * t), m1 = slots_below(16 * x + 8 + 2 * t);
+    auto below = [&](int key) { return key + 1 < held ? 0xFFFFFFFFu : (key < held ? 0xFFFFu : 0u); };
+    uint32_t m0 = 0, m1 = 0;
+    if (EDGE) {
+      m0 = below(16 * x + 2 * t);
+      m1 = below(16 * x + 8 + 2 * t);
+    }
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
       uint32_t va[4];
-      ldmatrix_trans(row + (c >> 2) * C::HALF_BYTES + ((((c & 3) * 2 + (m8 & 1)) ^ l7) << 4), va);
-      if (edge) {
+      ldmatrix_trans(stage + lanes.v[c & 3] + x * 2048 + (c >> 2) * HALF_BYTES, va);
+      if (EDGE) {
         va[0] &= m0;
         va[1] &= m0;
         va[2] &= m1;
@@ -492,8 +510,8 @@ __device__ __forceinline__ void attend_slots(uint32_t kt, uint32_t vt, const uin
       for (int n = 0; n < NT; ++n) N::mma(acc.o[c][n], va, lo[n][0], lo[n][1]);
     }
   }
-  if (odd)
-    for (int key = 0; key < min(C::KEYS, held); ++key)
+  if (EDGE && odd)
+    for (int key = 0; key < min(KEYS, held); ++key)
 #pragma unroll
       for (int c = 0; c < D / 16; ++c)
 #pragma unroll
@@ -534,30 +552,30 @@ struct Sink {
 };
 
 template <int D, int NT, typename T, bool MASS>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(32 * MAX_WARPS, 1)
 attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const Args a,
               const Shape s, const T *__restrict__ q, const Sink<D, T> sink, const Work work, long long limit) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
-  constexpr int STAGES = RING_BYTES / STAGE_BYTES;
-  __shared__ uint64_t full[STAGES], empty[STAGES];  // worker after worker
-  __shared__ Piece pieces[STAGES];
-  __shared__ int warp_units[WARPS];
-  __shared__ int begin[WARPS][2];  // row each worker begins in, units of it before
+  __shared__ uint64_t full[MAX_STAGES], empty[MAX_STAGES];  // worker after worker
+  __shared__ Piece pieces[MAX_STAGES];
+  __shared__ int warp_units[MAX_WARPS];
+  __shared__ int begin[MAX_WARPS][2];  // row each worker begins in, units of it before
   __shared__ uint32_t abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rows = a.B * a.H, M = s.group * s.n_q;
-  const int tiles = tiles_of(M), workers = workers_of(M), stages = STAGES / workers;
+  const int tiles = tiles_of(M), workers = workers_of(M), stages = C::stages(M);
+  const int threads = blockDim.x;
   const int wk = warp / tiles, mt = warp % tiles, g = lane >> 2, t = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid < STAGES) {
+  if (tid < workers * stages) {
     tc::mbar_init(&full[tid], 1);
     tc::mbar_init(&empty[tid], tiles);
     tc::fence_barrier_init();
   }
   if (tid == 0) abort = 0u;
   // units before each thread's rows; rows without pages get their zeros here
-  const int per = (rows + THREADS - 1) / THREADS;
+  const int per = (rows + threads - 1) / threads;
   const int lo = (int)min((long long)rows, (long long)tid * per), hi = min(rows, lo + per);
   int mine = 0;
   for (int r = lo; r < hi; ++r) {
@@ -570,7 +588,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
   __syncthreads();
   int units = 0, before = upto - mine;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
+  for (int w = 0; w < MAX_WARPS; ++w) {
+    if (32 * w >= threads) break;
     if (w < warp) before += warp_units[w];
     units += warp_units[w];
   }
@@ -602,7 +621,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
   if (u0 >= u1) return;
 
   Producer<D> p;
-  p.ring = smem_raw + (1024 - (tc::smem_u32(smem_raw) & 1023u)) + wk * stages * STAGE_BYTES;
+  p.ring = smem_raw + (1024 - (tc::smem_u32(smem_raw) & 1023u)) + wk * stages * C::STAGE_BYTES;
   p.full = full + wk * stages;
   p.empty = empty + wk * stages;
   p.piece = pieces + wk * stages;
@@ -627,29 +646,43 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
   bool ok = true;
   Tile<D, NT> acc;
   uint32_t qb[NT][D / 16][2];
+  Lanes lanes;
+  lanes.init<D>();
+  const uint32_t ring = tc::smem_u32(p.ring);
   int stage = 0, parity = 0;
   for (int it = 0;; ++it) {
     if (mt == 0)
       while (p.ok && !p.ended && p.issued < it + stages)
-        p.send(tk, tv, a, s, rows, split, MASS ? work.units : nullptr, &abort, limit);
+        p.send(tk, tv, a, s, rows, split, work.units, &abort, limit);
+    if (!p.ok) {
+      ok = false;
+      break;
+    }
+    // The warp that sent the piece knows it already, and has the queries of a
+    // new row on their way while it waits for the keys.
+    __syncwarp();
+    Piece d = p.piece[stage];
+    if (mt == 0 && (d.flags & FIRST)) load_queries<D, NT, T>(q, a, s, d.row, m0, qb);
     ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&p.full[stage], parity, &abort, limit));
     if (!ok) break;
-    const Piece d = p.piece[stage];
-    if (d.flags & FIRST) {
-      load_queries<D, NT, T>(q, a, s, d.row, m0, qb);
-      acc.clear();
+    if (mt != 0) {
+      d = p.piece[stage];
+      if (d.flags & FIRST) load_queries<D, NT, T>(q, a, s, d.row, m0, qb);
     }
+    if (d.flags & FIRST) acc.clear();
     if (!(d.flags & SKIP) && tile_rows > 0) {
       int lim[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int y = 0; y < 2; ++y) lim[n][y] = d.held - back[n][y];
-      const uint32_t kt = tc::smem_u32(p.ring + stage * STAGE_BYTES);
+      const uint32_t at = ring + stage * C::STAGE_BYTES;
       float *sc = nullptr;
-      if (MASS) sc = work.scores + ((long long)d.unit * M + m0) * PAGE + (d.flags >> SUB_SHIFT) * C::KEYS;
-      attend_slots<D, NT, T, MASS>(kt, kt + C::TILE_BYTES, qb, s, lim, d.held, d.held - (s.n_q - 1) < C::KEYS, acc, sc,
-                                   tile_rows);
+      if (MASS) sc = work.scores + ((long long)d.unit * M + m0) * PAGE + (d.flags >> SUB_SHIFT) * KEYS;
+      if (d.held - (s.n_q - 1) < KEYS)
+        attend_slots<D, NT, T, MASS, true>(at, lanes, qb, s, lim, d.held, acc, sc, tile_rows);
+      else
+        attend_slots<D, NT, T, MASS, false>(at, lanes, qb, s, lim, d.held, acc, sc, tile_rows);
     }
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&p.empty[stage]);
@@ -712,9 +745,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
       tc::mbar_wait(&p.full[x % stages], (x / stages) & 1, nullptr, DRAIN_LIMIT);
 }
 
-// grid.x = the workers of attend_kernel; grid.y shares out each one's units.
 constexpr int JOIN_THREADS = 128;
-constexpr int JOIN_SHARES = 4;
 
 // (maximum, sum) of two parts of a sum of exponentials; a sum of 0 is nothing.
 __device__ __forceinline__ float2 join_two(float2 x, float2 y) {
@@ -724,14 +755,16 @@ __device__ __forceinline__ float2 join_two(float2 x, float2 y) {
   return make_float2(top, x.y * tc::ex2(x.x - top) + y.y * tc::ex2(y.x - top));
 }
 
-template <int D, typename T, bool MASS>
+// grid.x = the workers of attend_kernel: the outputs of a row in parts are
+// shared out among the CTAs of its workers.
+template <int D, typename T>
 __global__ void __launch_bounds__(JOIN_THREADS)
 join_kernel(const Args a, const Shape s, const Sink<D, T> sink, const Work work) {
   constexpr int W = JOIN_THREADS / 32;
-  __shared__ float row_lse[2][MAX_ROWS];
   __shared__ float2 row_ml[MAX_ROWS];  // maximum, 1 / sum
   __shared__ float2 warp_ml[W];
   __shared__ float4 warp_o[W][32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, M = s.group * s.n_q;
   const int worker = blockIdx.x;
@@ -742,20 +775,18 @@ join_kernel(const Args a, const Shape s, const Sink<D, T> sink, const Work work)
     if (r < 0) continue;
     const int w0 = cache::first_worker(split.start[x], split.chunk);
     const int parts = cache::last_worker(split.start[x], split.pages[x], split.chunk) - w0 + 1;
-    // The row's outputs, four to an element, are shared out among its workers:
-    // `each` elements to a CTA, from element e0 on.
-    const int elements = M * (D / 4), ctas = parts * (int)gridDim.y;
-    const int each = max(2, (elements + ctas - 1) / ctas);
-    const int e0 = min(elements, ((worker - w0) * (int)gridDim.y + (int)blockIdx.y) * each);
-    const int e1 = min(elements, e0 + each);
-    // maximum and sum of the query rows that this CTA needs
-    const int ma = MASS ? 0 : e0 / (D / 4), mb = MASS ? M : (e1 + D / 4 - 1) / (D / 4);
+    // four outputs to an element; `each` elements to a CTA, from e0 on
+    const int elements = M * (D / 4), each = max(2, (elements + parts - 1) / parts);
+    const int e0 = min(elements, (worker - w0) * each), e1 = min(elements, e0 + each);
+    // the query rows whose maximum and sum this CTA needs
+    const int ma = e0 / (D / 4), mb = (e1 + D / 4 - 1) / (D / 4);
     auto part = [&](int k, int m) { return (long long)cache::part_of(w0 + k, k == 0) * M + m; };
     auto put = [&](int m, float2 ml) {
       const float y = ml.y == 0.0f ? -INFINITY : ml.x + log2f(ml.y);
-      row_lse[x][m] = y;
       row_ml[m] = make_float2(ml.x, ml.y == 0.0f ? 0.0f : 1.0f / ml.y);
-      if (m * (D / 4) >= e0 && m * (D / 4) < e1) sink.put_lse(a, s, r, m, y);
+      if (m * (D / 4) < e0) return;  // another CTA's first element
+      sink.put_lse(a, s, r, m, y);
+      if (work.lse2 != nullptr) work.lse2[(long long)r * M + m] = y;
     };
     auto over_warp = [&](float2 ml) {
 #pragma unroll
@@ -839,26 +870,42 @@ join_kernel(const Args a, const Shape s, const Sink<D, T> sink, const Work work)
       }
     }
   }
-  if (MASS) {
-    __syncthreads();
-    const int rows = a.B * a.H;
-    const int u1 = cache::chunk_begin(worker + 1, split.chunk, split.units);
-    const int j = tid % PAGE;
-    for (int u = cache::chunk_begin(worker, split.chunk, split.units) + (int)blockIdx.y * (JOIN_THREADS / PAGE) +
-                 tid / PAGE;
-         u < u1; u += (int)gridDim.y * (JOIN_THREADS / PAGE)) {
-      const int2 at = work.units[u];
-      if (at.x < 0 || at.x >= rows || at.y < 0 || at.y >= a.max_pages) continue;
-      if (at.y * PAGE + j >= a.lens[at.x]) continue;  // behind the last slot
-      const float *lse = at.x == split.row[0] ? row_lse[0] : (at.x == split.row[1] ? row_lse[1] : nullptr);
+}
+
+constexpr int WEIGH_THREADS = 256;
+constexpr int WEIGH_PAGES = WEIGH_THREADS / PAGE;  // of a CTA at a time
+
+// A thread per slot; the grid strides over the pages.
+__global__ void __launch_bounds__(WEIGH_THREADS)
+weigh_kernel(const Args a, const int M, const Work work) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int rows = a.B * a.H, units = work.split[0].units;
+  const int j = threadIdx.x % PAGE, step = (int)gridDim.x * WEIGH_PAGES;
+  int u = (int)blockIdx.x * WEIGH_PAGES + (int)threadIdx.x / PAGE;
+  int2 at = u < units ? work.units[u] : make_int2(-1, -1);
+  for (; u < units; u += step) {
+    const int2 next = u < units - step ? work.units[u + step] : make_int2(-1, -1);
+    const int col = at.y & 0xFFFFFF;
+    // (the bounds hold for whatever a call that was given up has left here)
+    if (at.x >= 0 && at.x < rows && at.y >= 0 && col < a.max_pages && j <= at.y >> 24) {
+      const float *x = work.scores + (long long)u * M * PAGE + j, *y = work.lse2 + (long long)at.x * M;
+      float *w = a.weight + a.slot(at.x, col * PAGE + j);
+      const float old = *w;
       float got = 0.0f;
-      for (int m = 0; m < M; ++m) {
-        const float y = lse != nullptr ? lse[m] : work.lse2[(long long)at.x * M + m];
-        const float x = work.scores[((long long)u * M + m) * PAGE + j];
-        if (y != -INFINITY) got += tc::ex2(x - y);
+      for (int m0 = 0; m0 < M; m0 += 8) {
+        float xs[8], ys[8];
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          xs[m] = m0 + m < M ? x[(m0 + m) * PAGE] : -INFINITY;
+          ys[m] = m0 + m < M ? y[m0 + m] : 0.0f;
+        }
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+          if (ys[m] != -INFINITY) got += tc::ex2(xs[m] - ys[m]);  // else the query sees nothing
       }
-      if (got != 0.0f) a.weight[a.slot(at.x, at.y * PAGE + j)] += got;
+      if (got != 0.0f) *w = old + got;
     }
+    at = next;
   }
 }
 

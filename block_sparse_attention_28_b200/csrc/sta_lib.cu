@@ -500,39 +500,45 @@ sta_status launch_decode(const sta_kv_cache *c, const cache::Args &a, const deco
   work.part_o = reinterpret_cast<float *>(ws + w.part_o);
   work.part_ml = reinterpret_cast<float2 *>(ws + w.part_ml);
   work.split = reinterpret_cast<decode::Split *>(ws + w.split);
-  work.units = reinterpret_cast<int2 *>(ws + w.units);
-  work.scores = reinterpret_cast<float *>(ws + w.scores);
-  work.lse2 = reinterpret_cast<float *>(ws + w.lse2);
+  work.units = MASS ? reinterpret_cast<int2 *>(ws + w.units) : nullptr;
+  work.scores = MASS ? reinterpret_cast<float *>(ws + w.scores) : nullptr;
+  work.lse2 = MASS ? reinterpret_cast<float *>(ws + w.lse2) : nullptr;
   decode::Sink<D, T> sink;
   sink.o = static_cast<T *>(o);
   sink.lse = lse;
   CUtensorMap tk, tv;
   const unsigned long long pool_rows = (unsigned long long)c->num_pages * c->kv_heads * cache::PAGE;
-  if (!make_tile_map(&tk, c->k_pages, pool_rows, D, C::KEYS) ||
-      !make_tile_map(&tv, c->v_pages, pool_rows, D, C::KEYS))
+  if (!make_tile_map(&tk, c->k_pages, pool_rows, D, decode::KEYS) ||
+      !make_tile_map(&tv, c->v_pages, pool_rows, D, decode::KEYS))
     return STA_ERR_CUDA;
   auto attend = decode::attend_kernel<D, NT, T, MASS>;
-  STA_CUDA_TRY(cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+  STA_CUDA_TRY(cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(M)));
   const long long most = (long long)c->B * c->kv_heads * c->max_pages;
   const int sms = sm100_count() < decode::MAX_CTAS ? sm100_count() : decode::MAX_CTAS;
   const unsigned ctas = (unsigned)(most < sms ? most : sms);
   const int workers = decode::workers_of(M);
-  attend<<<ctas, decode::THREADS, C::SMEM, s>>>(tk, tv, a, shape, static_cast<const T *>(q), sink, work, wait_limit());
+  attend<<<ctas, 32 * decode::warps_of(M), C::smem(M), s>>>(tk, tv, a, shape, static_cast<const T *>(q), sink, work, wait_limit());
   STA_CUDA_TRY(cudaGetLastError());
-  // The join may start up while attend_kernel runs; it waits for its end
-  // before it reads anything.
+  // Each kernel may start up while the one before it runs; it waits for that
+  // one's end before it reads anything.
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas * workers, MASS ? decode::JOIN_SHARES : 1);
+  cfg.gridDim = dim3(ctas * workers);
   cfg.blockDim = dim3(decode::JOIN_THREADS);
   cfg.stream = s;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  STA_CUDA_TRY(cudaLaunchKernelEx(&cfg, decode::join_kernel<D, T, MASS>, a, shape,
+  STA_CUDA_TRY(cudaLaunchKernelEx(&cfg, decode::join_kernel<D, T>, a, shape,
                                   static_cast<const decode::Sink<D, T>>(sink),
                                   static_cast<const decode::Work>(work)));
+  if (MASS) {
+    const long long pages = (most + decode::WEIGH_PAGES - 1) / decode::WEIGH_PAGES;
+    cfg.gridDim = dim3((unsigned)(pages < 8 * sms ? pages : 8 * sms));  // at most what an SM holds
+    cfg.blockDim = dim3(decode::WEIGH_THREADS);
+    STA_CUDA_TRY(cudaLaunchKernelEx(&cfg, decode::weigh_kernel, a, M, static_cast<const decode::Work>(work)));
+  }
   return STA_OK;
 }
 

@@ -31,24 +31,26 @@ STA_HD bool column_ok(int column, int before, int filled) {
 
 // Work is counted in units, rows one after another: a row of n pages has
 // ROW_COST units for itself (its queries, its result) and one for each page; a
-// row without pages has none. Units are cut into equal chunks, one per worker;
-// a row cut by a chunk border is summed up in parts and joined afterwards.
+// row without pages has none. The units are cut into equal chunks, one per
+// worker; a row cut by a chunk border is summed up in parts and joined
+// afterwards.
 constexpr int ROW_COST = 1;
 STA_HD int row_units(int pages) { return pages > 0 ? pages + ROW_COST : 0; }
-STA_HD int chunk_units(int units, int workers) {
+struct Chunks {
+  int units, size;
+  STA_HD int begin(int c) const {
+    const long long u = (long long)c * size;
+    return u < units ? (int)u : units;
+  }
+  STA_HD int of(int unit) const { return unit / size; }  // the chunk a unit lies in
+};
+STA_HD Chunks make_chunks(int units, int workers) {
   const int even = (int)(((long long)units + workers - 1) / workers);
-  return even > 1 ? even : 1;
+  return Chunks{units, even > 1 ? even : 1};
 }
-STA_HD int chunk_begin(int worker, int chunk, int units) {
-  const long long u = (long long)worker * chunk;
-  return u < units ? (int)u : units;
-}
-// The workers that hold pages of a row whose first page is unit `start`.
-STA_HD int first_worker(int start, int chunk) { return start / chunk; }
-STA_HD int last_worker(int start, int pages, int chunk) { return (int)(((long long)start + pages - 1) / chunk); }
-// Where a worker leaves its part of a row that it does not hold whole. It has
-// two such rows at most: the one it goes on with and the one it begins.
-STA_HD int part_of(int worker, bool begins) { return 2 * worker + (begins ? 1 : 0); }
+// Where a chunk's part of a row lies that it does not hold whole. It has two
+// such rows at most: the one it goes on with and the one it begins.
+STA_HD int part_of(int chunk, bool begins) { return 2 * chunk + (begins ? 1 : 0); }
 
 }  // namespace cache
 }  // namespace sta

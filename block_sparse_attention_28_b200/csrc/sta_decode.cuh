@@ -10,15 +10,15 @@
 // and 8 query rows across: S^T = K Q^T, O^T = V^T P^T. (A tcgen05 tile has 64
 // rows at least; a token of a group of 1 to 8 heads has 8 to offer.)
 //
-// attend_kernel: one CTA per SM, 8 warps. A worker is a warp (two or four for
-// more than 16 or 32 query rows, 16 each) with a ring of its own in shared
-// memory, into which its first warp sends pieces of pages (TMA, 128-byte
-// swizzle) ahead of their use. The pages to be read, rows one after another,
-// are cut into one equal chunk per worker whatever the lengths are: no worker
-// waits for a long sequence, or for another where a row ends. Each warp keeps
-// the running maximum and sum and the outputs of its query rows in registers;
-// rows cut by a chunk border leave their parts (the sum relative to a maximum)
-// in the workspace.
+// attend_kernel: one CTA per SM, 7 or 8 warps. A worker is a warp (two or four
+// for more than 16 or 32 query rows, 16 each) with a ring of its own in shared
+// memory, into which its first warp sends half pages (TMA, 128-byte swizzle)
+// ahead of their use. The pages to be read, rows one after another, are cut
+// into one equal chunk per worker whatever the lengths are: no worker waits for
+// a long sequence, or for another where a row ends. Each warp keeps the running
+// maximum and sum and the outputs of its query rows in registers; rows cut by a
+// chunk border leave their parts (the sum relative to a maximum) in the
+// workspace.
 // join_kernel: joins those parts.
 // weigh_kernel: adds every slot's attention to its weight now that the rows'
 // log-sum-exps are known, from the scores that attend_kernel left (4 bytes per
@@ -67,18 +67,11 @@ struct Shape {
   float scale_log2;  // scale * log2 e
 };
 
-// A worker's rows that it does not hold whole (row -1: none): [0] the one it
-// goes on with, [1] the one it begins; the unit of the row's first page, and
-// its pages.
-struct Split {
-  int row[2], start[2], pages[2];
-  int chunk, units;
-};
-
 struct Work {
-  float *part_o;      // [2 * workers][M][D]
-  float2 *part_ml;    // [2 * workers][M] maximum (log2) and sum
-  Split *split;       // [workers]
+  float *part_o;      // [2 * chunks][M][D]
+  float2 *part_ml;    // [2 * chunks][M] maximum (log2) and sum
+  int2 *row_units;    // [rows] unit of the first page and pages of a row in parts; pages 0: not in parts
+  cache::Chunks *chunks;
   // for weigh_kernel (else NULL)
   int2 *units;        // [units] row, and packed column and filled slots, of a page; else -1
   float *scores;      // [units][M][PAGE] s_j log2 e, -inf out of view
@@ -89,11 +82,11 @@ struct Work {
 __device__ __forceinline__ int pack_page(int col, int held) { return col | (min(held, PAGE) - 1) << 24; }
 
 // What a worker's warps are told of a stage.
-enum : int { FIRST = 1, LAST = 2, WHOLE = 4, BEGINS = 8, SKIP = 16, END = 32, SUB_SHIFT = 8 };
+enum : int { FIRST = 1, LAST = 2, WHOLE = 4, BEGINS = 8, SKIP = 16, END = 32, UPPER = 64 };
 struct __align__(16) Piece {
   int row, unit;
   int held;   // filled slots from the piece's first on (may be above KEYS)
-  int flags;  // and, from SUB_SHIFT on, which piece of its page it is
+  int flags;  // UPPER: the page's second half
 };
 
 // ------------------------------------------------------------ element types
@@ -189,32 +182,39 @@ struct Producer {
   uint64_t *full, *empty;
   Piece *piece;
   int stages;
-  int row, off;   // the next unit's row, units of the row before it
-  int u, u0, u1;  // the next unit, the worker's range
+  int row, off;   // a row and the next unit to be looked up, counted from the row's first
+  int u, u0, u1;  // that unit, the chunk's range
   int issued;     // stages sent
   bool ended, ok;
   // this lane's unit of the batch at hand
   int w_row, w_unit, w_held, w_flags, w_y;
   unsigned left;  // lanes of the batch still to be sent
-  int sub;        // pieces of the first of them that are sent
+  int upper;      // 1: the first of them has its lower half sent
 
-  // Looks up the next 32 units.
-  __device__ __forceinline__ void batch(const Args &a, const Shape &s, int rows, Split *split, int2 *units) {
-    static_assert(cache::ROW_COST == 1, "what is the worker's last page");
+  // Looks up the next units of the chunk, 32 at most.
+  __device__ __forceinline__ void batch(const Args &a, const Shape &s, int rows, const Work &work) {
+    static_assert(cache::ROW_COST == 1, "what is the chunk's last page");
     const int lane = threadIdx.x & 31;
     const int r0 = row + lane;
     RowPages mine = {0, 0, 0};
     if (r0 < rows) mine = row_pages(a, s, r0);
-    const int upto = cache::warp_scan(cache::row_units(mine.n) - (lane == 0 ? off : 0));
+    const int upto = cache::warp_scan(cache::row_units(mine.n));
     const int total = __shfl_sync(0xFFFFFFFFu, upto, 31);
-    const int take = min(min(total, u1 - u), 32);
-    int k = 0;  // the row of this lane's unit: the first with upto > lane
+    left = 0;
+    upper = 0;
+    if (off >= total) {  // not in these 32 rows
+      row += 32;
+      off -= total;
+      return;
+    }
+    const int take = min(min(total - off, u1 - u), 32), at = off + lane;
+    int k = 0;  // the row of this lane's unit: the first with upto > at
 #pragma unroll
     for (int step = 16; step > 0; step >>= 1)
-      if (__shfl_sync(0xFFFFFFFFu, upto, k + step - 1) <= lane) k += step;
+      if (__shfl_sync(0xFFFFFFFFu, upto, k + step - 1) <= at) k += step;
     const int n = __shfl_sync(0xFFFFFFFFu, mine.n, k), first = __shfl_sync(0xFFFFFFFFu, mine.first, k);
     const int len = __shfl_sync(0xFFFFFFFFu, mine.len, k), end = __shfl_sync(0xFFFFFFFFu, upto, k);
-    const int i = n - (end - lane);  // the row's i-th page; negative: the row's own unit
+    const int i = n - (end - at);  // the row's i-th page; negative: the row's own unit
     const bool page_unit = lane < take && i >= 0;
     w_row = row + k;
     w_unit = u + lane;
@@ -244,51 +244,44 @@ struct Producer {
       // a row's own unit follows its last page, if anything does
       if (w_unit == u1 - 1 || (i == n - 1 && w_unit == u1 - 2)) w_flags |= END;
       if (begins) w_flags |= BEGINS;
-      if (begins && start + n <= u1) {
-        w_flags |= WHOLE;
-      } else if (w_flags & FIRST) {
-        split->row[begins] = w_row;
-        split->start[begins] = start;
-        split->pages[begins] = n;
-      }
+      if (begins && start + n <= u1) w_flags |= WHOLE;
+      if (i == 0) work.row_units[w_row] = make_int2(start, w_flags & WHOLE ? 0 : n);
     }
-    if (units != nullptr && lane < take)
-      units[w_unit] = col >= 0 ? make_int2(w_row, pack_page(col, w_held)) : make_int2(-1, -1);
+    if (work.units != nullptr && lane < take)
+      work.units[w_unit] = col >= 0 ? make_int2(w_row, pack_page(col, w_held)) : make_int2(-1, -1);
     left = __ballot_sync(0xFFFFFFFFu, page_unit);
-    sub = 0;
-    if (take > 0) {  // the unit after the batch
-      u += take;
-      const int lk = __shfl_sync(0xFFFFFFFFu, k, take - 1), le = __shfl_sync(0xFFFFFFFFu, end, take - 1);
-      const int ln = __shfl_sync(0xFFFFFFFFu, n, take - 1);
-      off = cache::row_units(ln) - (le - take);  // of row row + lk, its last unit included
-      row += lk;
-    } else {
-      row += 32;  // 32 rows without pages
-      off = 0;
-    }
+    // the unit after these, counted from the last one's row
+    const int lk = __shfl_sync(0xFFFFFFFFu, k, take - 1), le = __shfl_sync(0xFFFFFFFFu, end, take - 1);
+    const int ln = __shfl_sync(0xFFFFFFFFu, n, take - 1);
+    u += take;
+    off += take - (le - cache::row_units(ln));
+    row += lk;
   }
 
-  // Sends the next piece.
+  // Looks up units until there is a page among them.
+  __device__ __forceinline__ void find(const Args &a, const Shape &s, int rows, const Work &work) {
+    while (left == 0 && u < u1 && row < rows) batch(a, s, rows, work);
+  }
+
+  // Sends the next piece; where a chunk has no page, just the end.
   __device__ __forceinline__ void send(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, const Shape &s,
-                                       int rows, Split *split, int2 *units, volatile uint32_t *abort,
-                                       long long limit) {
-    while (left == 0 && u < u1 && row < rows) batch(a, s, rows, split, units);
+                                       int rows, const Work &work, volatile uint32_t *abort, long long limit) {
     const int lane = threadIdx.x & 31, stage = issued % stages;
-    const bool none = left == 0;  // nothing but a row's own unit in the whole range
+    const bool none = left == 0;
     const int x = none ? 0 : __ffs(left) - 1;
     int state = 0;
     if (lane == x) {
-      const bool last = none || (w_flags & SKIP) || w_held <= (sub + 1) * KEYS || (sub + 1) * KEYS == PAGE;
-      int flags = none ? (SKIP | END) : w_flags | sub << SUB_SHIFT;
-      if (sub > 0) flags &= ~FIRST;
+      const bool last = none || (w_flags & SKIP) || upper || w_held <= KEYS;
+      int flags = none ? (SKIP | END) : w_flags;
+      if (upper) flags = (flags & ~FIRST) | UPPER;
       if (!last) flags &= ~(LAST | END);
       if (issued < stages || tc::mbar_wait(&empty[stage], ((issued / stages) & 1) ^ 1, abort, limit)) {
-        piece[stage] = Piece{w_row, w_unit, w_held - sub * KEYS, flags};
+        piece[stage] = Piece{w_row, w_unit, w_held - upper * KEYS, flags};
         if (flags & SKIP) {
           tc::mbar_arrive(&full[stage]);
         } else {
           const uint32_t dst = tc::smem_u32(ring + stage * C::STAGE_BYTES);
-          const int y = w_y + sub * KEYS;
+          const int y = w_y + upper * KEYS;
           tc::mbar_expect_tx(&full[stage], C::STAGE_BYTES);
 #pragma unroll
           for (int e = 0; e < D / 64; ++e) tc::tma_load_2d(dst + e * HALF_BYTES, &tk, &full[stage], 64 * e, y);
@@ -300,13 +293,15 @@ struct Producer {
       }
     }
     state = __shfl_sync(0xFFFFFFFFu, state, x);
-    ok = state & 1;
+    ok = state != 0;
     ended = state & END;
     if (ok) ++issued;
-    ++sub;
     if (state & 2) {
-      sub = 0;
+      upper = 0;
       left &= left - 1;
+      find(a, s, rows, work);  // while what was sent is on its way
+    } else {
+      upper = 1;
     }
   }
 };
@@ -560,7 +555,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
   __shared__ uint64_t full[MAX_STAGES], empty[MAX_STAGES];  // worker after worker
   __shared__ Piece pieces[MAX_STAGES];
   __shared__ int warp_units[MAX_WARPS];
-  __shared__ int begin[MAX_WARPS][2];  // row each worker begins in, units of it before
+  __shared__ int row_before[32 * MAX_WARPS];  // units before the rows of each thread
   __shared__ uint32_t abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rows = a.B * a.H, M = s.group * s.n_q;
@@ -573,7 +568,11 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
     tc::mbar_init(&empty[tid], tiles);
     tc::fence_barrier_init();
   }
-  if (tid == 0) abort = 0u;
+  if (tid == 0) {
+    abort = 0u;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tk) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tv) : "memory");
+  }
   // units before each thread's rows; rows without pages get their zeros here
   const int per = (rows + threads - 1) / threads;
   const int lo = (int)min((long long)rows, (long long)tid * per), hi = min(rows, lo + per);
@@ -581,7 +580,10 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
   for (int r = lo; r < hi; ++r) {
     const int n = row_pages(a, s, r).n;
     mine += cache::row_units(n);
-    if (n == 0 && r % gridDim.x == blockIdx.x) sink.put_nothing(a, s, r);
+    if (n == 0 && r % gridDim.x == blockIdx.x) {
+      sink.put_nothing(a, s, r);
+      work.row_units[r] = make_int2(0, 0);
+    }
   }
   const int upto = cache::warp_scan(mine);
   if (lane == 31) warp_units[warp] = upto;
@@ -593,47 +595,33 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
     if (w < warp) before += warp_units[w];
     units += warp_units[w];
   }
-  // few units: a worker of every SM before a second one of any
-  const int chunk = cache::chunk_units(units, workers * gridDim.x);
-  for (int w = 0; w < workers; ++w) {
-    const int u0 = cache::chunk_begin(w * gridDim.x + blockIdx.x, chunk, units);
-    if (u0 < units && before <= u0 && u0 < before + mine) {
-      int at = before, r = lo;
-      for (; r < hi; ++r) {
-        const int n = cache::row_units(row_pages(a, s, r).n);
-        if (u0 < at + n) break;
-        at += n;
-      }
-      begin[w][0] = r;
-      begin[w][1] = u0 - at;
-    }
-  }
+  row_before[tid] = before;
   __syncthreads();
-  const int worker = wk * gridDim.x + blockIdx.x;
-  const int u0 = cache::chunk_begin(worker, chunk, units), u1 = cache::chunk_begin(worker + 1, chunk, units);
-  Split *split = work.split + worker;
-  if (mt == 0 && lane == 0) {
-    split->row[0] = split->row[1] = -1;
-    split->chunk = chunk;
-    split->units = units;
-  }
-  __syncwarp();
-  if (u0 >= u1) return;
+  const cache::Chunks chunks = cache::make_chunks(units, workers * gridDim.x);
+  if (tid == 0 && blockIdx.x == 0) *work.chunks = chunks;
 
+  // few units: a worker of every SM before a second one of any
+  const int worker = wk * gridDim.x + blockIdx.x;
   Producer<D> p;
+  p.u = p.u0 = chunks.begin(worker);
+  p.u1 = chunks.begin(worker + 1);
+  if (p.u0 >= p.u1) return;
   p.ring = smem_raw + (1024 - (tc::smem_u32(smem_raw) & 1023u)) + wk * stages * C::STAGE_BYTES;
   p.full = full + wk * stages;
   p.empty = empty + wk * stages;
   p.piece = pieces + wk * stages;
   p.stages = stages;
-  p.row = begin[wk][0];
-  p.off = begin[wk][1];
-  p.u = p.u0 = u0;
-  p.u1 = u1;
-  p.issued = p.sub = 0;
+  p.issued = p.upper = 0;
+  p.left = 0;
   p.ended = false;
   p.ok = true;
-  p.left = 0;
+  if (mt == 0) {
+    int n = 0;  // threads whose rows begin at or before the chunk
+    for (int i = 0; i < threads; i += 32) n += __popc(__ballot_sync(0xFFFFFFFFu, row_before[i + lane] <= p.u0));
+    p.row = (n - 1) * per;
+    p.off = p.u0 - row_before[n - 1];
+    p.find(a, s, rows, work);
+  }
   const int m0 = 16 * mt, tile_rows = min(8 * NT, M - m0);  // may be <= 0
   int back[NT][2];  // newer tokens than the query row's
 #pragma unroll
@@ -652,8 +640,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
   int stage = 0, parity = 0;
   for (int it = 0;; ++it) {
     if (mt == 0)
-      while (p.ok && !p.ended && p.issued < it + stages)
-        p.send(tk, tv, a, s, rows, split, work.units, &abort, limit);
+      while (p.ok && !p.ended && p.issued < it + stages) p.send(tk, tv, a, s, rows, work, &abort, limit);
     if (!p.ok) {
       ok = false;
       break;
@@ -678,7 +665,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
         for (int y = 0; y < 2; ++y) lim[n][y] = d.held - back[n][y];
       const uint32_t at = ring + stage * C::STAGE_BYTES;
       float *sc = nullptr;
-      if (MASS) sc = work.scores + ((long long)d.unit * M + m0) * PAGE + (d.flags >> SUB_SHIFT) * KEYS;
+      if (MASS) sc = work.scores + ((long long)d.unit * M + m0) * PAGE + (d.flags & UPPER ? KEYS : 0);
       if (d.held - (s.n_q - 1) < KEYS)
         attend_slots<D, NT, T, MASS, true>(at, lanes, qb, s, lim, d.held, acc, sc, tile_rows);
       else
@@ -747,128 +734,70 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
 
 constexpr int JOIN_THREADS = 128;
 
-// (maximum, sum) of two parts of a sum of exponentials; a sum of 0 is nothing.
-__device__ __forceinline__ float2 join_two(float2 x, float2 y) {
-  if (y.y == 0.0f) return x;
-  if (x.y == 0.0f) return y;
-  const float top = fmaxf(x.x, y.x);
-  return make_float2(top, x.y * tc::ex2(x.x - top) + y.y * tc::ex2(y.x - top));
-}
+// A part of a row's sum: the weights' maximum (log2) and sum, four outputs. A
+// sum of 0 is nothing.
+struct Part {
+  float top, sum;
+  float4 o;
+  __device__ __forceinline__ void add(const Part &p) {
+    if (p.sum == 0.0f) return;
+    const float up = sum == 0.0f ? p.top : fmaxf(top, p.top);
+    const float x = sum == 0.0f ? 0.0f : tc::ex2(top - up), y = tc::ex2(p.top - up);
+    top = up;
+    sum = sum * x + p.sum * y;
+    o.x = o.x * x + p.o.x * y;
+    o.y = o.y * x + p.o.y * y;
+    o.z = o.z * x + p.o.z * y;
+    o.w = o.w * x + p.o.w * y;
+  }
+};
 
-// grid.x = the workers of attend_kernel: the outputs of a row in parts are
-// shared out among the CTAs of its workers.
+// grid.x = rows; grid.y shares out a row's outputs, four to an element. Lanes
+// run along `wide` elements (a power of two), the rest of the CTA along the
+// parts; those sums are added up by shuffles and through shared memory.
 template <int D, typename T>
 __global__ void __launch_bounds__(JOIN_THREADS)
-join_kernel(const Args a, const Shape s, const Sink<D, T> sink, const Work work) {
-  constexpr int W = JOIN_THREADS / 32;
-  __shared__ float2 row_ml[MAX_ROWS];  // maximum, 1 / sum
-  __shared__ float2 warp_ml[W];
-  __shared__ float4 warp_o[W][32];
+join_kernel(const Args a, const Shape s, const Sink<D, T> sink, const Work work, int wide) {
+  __shared__ Part parts[JOIN_THREADS];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, M = s.group * s.n_q;
-  const int worker = blockIdx.x;
-  const Split split = work.split[worker];
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int r = split.row[x];
-    if (r < 0) continue;
-    const int w0 = cache::first_worker(split.start[x], split.chunk);
-    const int parts = cache::last_worker(split.start[x], split.pages[x], split.chunk) - w0 + 1;
-    // four outputs to an element; `each` elements to a CTA, from e0 on
-    const int elements = M * (D / 4), each = max(2, (elements + parts - 1) / parts);
-    const int e0 = min(elements, (worker - w0) * each), e1 = min(elements, e0 + each);
-    // the query rows whose maximum and sum this CTA needs
-    const int ma = e0 / (D / 4), mb = (e1 + D / 4 - 1) / (D / 4);
-    auto part = [&](int k, int m) { return (long long)cache::part_of(w0 + k, k == 0) * M + m; };
-    auto put = [&](int m, float2 ml) {
-      const float y = ml.y == 0.0f ? -INFINITY : ml.x + log2f(ml.y);
-      row_ml[m] = make_float2(ml.x, ml.y == 0.0f ? 0.0f : 1.0f / ml.y);
-      if (m * (D / 4) < e0) return;  // another CTA's first element
-      sink.put_lse(a, s, r, m, y);
-      if (work.lse2 != nullptr) work.lse2[(long long)r * M + m] = y;
-    };
-    auto over_warp = [&](float2 ml) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        ml = join_two(ml, make_float2(__shfl_xor_sync(0xFFFFFFFFu, ml.x, o), __shfl_xor_sync(0xFFFFFFFFu, ml.y, o)));
-      return ml;
-    };
-    __syncthreads();  // the row before has been dealt with
-    if (mb - ma >= W || parts <= 32) {
-      for (int m = ma + warp; m < mb; m += W) {
-        float2 ml = make_float2(0.0f, 0.0f);
-        for (int k = lane; k < parts; k += 32) ml = join_two(ml, work.part_ml[part(k, m)]);
-        ml = over_warp(ml);
-        if (lane == 0) put(m, ml);
-      }
-    } else {
-      for (int m = ma; m < mb; ++m) {
-        float2 ml = make_float2(0.0f, 0.0f);
-        for (int k = tid; k < parts; k += JOIN_THREADS) ml = join_two(ml, work.part_ml[part(k, m)]);
-        ml = over_warp(ml);
-        if (lane == 0) warp_ml[warp] = ml;
-        __syncthreads();
-        if (tid == 0) {
-          for (int w = 1; w < W; ++w) ml = join_two(ml, warp_ml[w]);
-          put(m, ml);
-        }
-        __syncthreads();
-      }
-    }
-    __syncthreads();
-    auto add = [&](float4 &o, int e, int k) {
-      const long long at = part(k, e / (D / 4));
+  const int tid = threadIdx.x, M = s.group * s.n_q;
+  const cache::Chunks chunks = *work.chunks;
+  const int r = blockIdx.x, first = work.row_units[r].x, n = work.row_units[r].y;
+  // (the bounds hold for whatever a call that was given up has left here)
+  if (first < 0 || n < 1 || n > a.max_pages || first > chunks.units - n) return;
+  const int c0 = chunks.of(first), c1 = chunks.of(first + n - 1);
+  const int e = (int)blockIdx.y * wide + tid % wide, m = e / (D / 4);
+  Part sum = {0.0f, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+  if (m < M)
+#pragma unroll 4
+    for (int c = c0 + tid / wide; c <= c1; c += JOIN_THREADS / wide) {
+      const long long at = (long long)cache::part_of(c, c == c0) * M + m;
       const float2 ml = work.part_ml[at];
-      const float4 v = *reinterpret_cast<const float4 *>(work.part_o + at * D + e % (D / 4) * 4);
-      const float f = ml.y != 0.0f ? tc::ex2(ml.x - row_ml[e / (D / 4)].x) : 0.0f;
-      o.x += v.x * f;
-      o.y += v.y * f;
-      o.z += v.z * f;
-      o.w += v.w * f;
-    };
-    auto finish = [&](const float4 &o, int e) {
-      const int m = e / (D / 4);
-      const float z = row_ml[m].y;
-      *reinterpret_cast<uint2 *>(sink.o + sink.row(a, s, r, m) * D + e % (D / 4) * 4) =
-          make_uint2(Num<T>::pack(o.x * z, o.y * z), Num<T>::pack(o.z * z, o.w * z));
-    };
-    if (e1 - e0 > 32) {
-      for (int e = e0 + tid; e < e1; e += JOIN_THREADS) {
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int k = 0; k < parts; ++k) add(o, e, k);
-        finish(o, e);
-      }
-    } else if (e0 < e1) {
-      // few elements: lanes along them (a power of two), the parts over the
-      // rest of the CTA, summed up by shuffles and through shared memory
-      int wide = 2;
-      while (wide < e1 - e0) wide *= 2;
-      const int e = e0 + lane % wide;
-      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (e < e1)
-#pragma unroll 4
-        for (int k = tid / wide; k < parts; k += JOIN_THREADS / wide) add(o, e, k);
-      for (int d = wide; d < 32; d *= 2) {
-        o.x += __shfl_xor_sync(0xFFFFFFFFu, o.x, d);
-        o.y += __shfl_xor_sync(0xFFFFFFFFu, o.y, d);
-        o.z += __shfl_xor_sync(0xFFFFFFFFu, o.z, d);
-        o.w += __shfl_xor_sync(0xFFFFFFFFu, o.w, d);
-      }
-      if (lane < wide) warp_o[warp][lane] = o;
-      __syncthreads();
-      if (tid < e1 - e0) {
-        for (int w = 1; w < W; ++w) {
-          const float4 v = warp_o[w][tid];
-          o.x += v.x;
-          o.y += v.y;
-          o.z += v.z;
-          o.w += v.w;
-        }
-        finish(o, e);
-      }
+      sum.add(Part{ml.x, ml.y, *reinterpret_cast<const float4 *>(work.part_o + at * D + e % (D / 4) * 4)});
     }
+  for (int d = wide; d < 32; d *= 2) {
+    Part p;
+    p.top = __shfl_xor_sync(0xFFFFFFFFu, sum.top, d);
+    p.sum = __shfl_xor_sync(0xFFFFFFFFu, sum.sum, d);
+    p.o.x = __shfl_xor_sync(0xFFFFFFFFu, sum.o.x, d);
+    p.o.y = __shfl_xor_sync(0xFFFFFFFFu, sum.o.y, d);
+    p.o.z = __shfl_xor_sync(0xFFFFFFFFu, sum.o.z, d);
+    p.o.w = __shfl_xor_sync(0xFFFFFFFFu, sum.o.w, d);
+    sum.add(p);
+  }
+  parts[tid] = sum;
+  __syncthreads();
+  if (tid >= wide || m >= M) return;
+  const int step = max(wide, 32);
+  for (int k = tid + step; k < JOIN_THREADS; k += step) sum.add(parts[k]);
+  const float z = sum.sum == 0.0f ? 0.0f : 1.0f / sum.sum;
+  *reinterpret_cast<uint2 *>(sink.o + sink.row(a, s, r, m) * D + e % (D / 4) * 4) =
+      make_uint2(Num<T>::pack(sum.o.x * z, sum.o.y * z), Num<T>::pack(sum.o.z * z, sum.o.w * z));
+  if (e % (D / 4) == 0) {
+    const float y = sum.sum == 0.0f ? -INFINITY : sum.top + log2f(sum.sum);
+    sink.put_lse(a, s, r, m, y);
+    if (work.lse2 != nullptr) work.lse2[(long long)r * M + m] = y;
   }
 }
 
@@ -879,7 +808,7 @@ constexpr int WEIGH_PAGES = WEIGH_THREADS / PAGE;  // of a CTA at a time
 __global__ void __launch_bounds__(WEIGH_THREADS)
 weigh_kernel(const Args a, const int M, const Work work) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int rows = a.B * a.H, units = work.split[0].units;
+  const int rows = a.B * a.H, units = work.chunks->units;
   const int j = threadIdx.x % PAGE, step = (int)gridDim.x * WEIGH_PAGES;
   int u = (int)blockIdx.x * WEIGH_PAGES + (int)threadIdx.x / PAGE;
   int2 at = u < units ? work.units[u] : make_int2(-1, -1);

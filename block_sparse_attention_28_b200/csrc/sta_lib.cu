@@ -462,17 +462,17 @@ sta_status decode_sizes(const sta_kv_cache *c, int32_t q_heads, int32_t n_q, int
   return STA_OK;
 }
 
-// Workspace of the attention over a cache: per worker two parts of rows cut by
-// its chunk's borders and their description; with accumulation also, per page
+// Workspace of the attention over a cache: per chunk two parts of rows cut by
+// its borders and their description; with accumulation also, per page
 // read, its row and column and its scores, and each row's log-sum-exp.
 struct DecodeWs {
-  size_t part_o, part_ml, split, units, scores, lse2, total;
+  size_t part_o, part_ml, row_units, header, units, scores, lse2, total;
 };
 
 DecodeWs decode_ws_layout(const sta_kv_cache *c, int group, int n_q, bool accumulate) {
   const size_t M = (size_t)group * n_q, rows = (size_t)c->B * c->kv_heads;
-  const size_t workers = (size_t)decode::MAX_CTAS * decode::workers_of((int)M), parts = 2 * workers;
   const size_t units = accumulate ? rows * (c->max_pages + cache::ROW_COST) : 0;
+  const size_t parts = 2 * (size_t)decode::MAX_CTAS * decode::workers_of((int)M);
   DecodeWs w;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -482,7 +482,8 @@ DecodeWs decode_ws_layout(const sta_kv_cache *c, int group, int n_q, bool accumu
   };
   w.part_o = take(parts * M * c->d * sizeof(float));
   w.part_ml = take(parts * M * sizeof(float2));
-  w.split = take(workers * sizeof(decode::Split));
+  w.row_units = take(rows * sizeof(int2));
+  w.header = take(sizeof(cache::Chunks));
   w.units = take(units * sizeof(int2));
   w.scores = take(units * M * cache::PAGE * sizeof(float));
   w.lse2 = take(accumulate ? rows * M * sizeof(float) : 0);
@@ -499,7 +500,8 @@ sta_status launch_decode(const sta_kv_cache *c, const cache::Args &a, const deco
   decode::Work work;
   work.part_o = reinterpret_cast<float *>(ws + w.part_o);
   work.part_ml = reinterpret_cast<float2 *>(ws + w.part_ml);
-  work.split = reinterpret_cast<decode::Split *>(ws + w.split);
+  work.row_units = reinterpret_cast<int2 *>(ws + w.row_units);
+  work.chunks = reinterpret_cast<cache::Chunks *>(ws + w.header);
   work.units = MASS ? reinterpret_cast<int2 *>(ws + w.units) : nullptr;
   work.scores = MASS ? reinterpret_cast<float *>(ws + w.scores) : nullptr;
   work.lse2 = MASS ? reinterpret_cast<float *>(ws + w.lse2) : nullptr;
@@ -516,23 +518,28 @@ sta_status launch_decode(const sta_kv_cache *c, const cache::Args &a, const deco
   const long long most = (long long)c->B * c->kv_heads * c->max_pages;
   const int sms = sm100_count() < decode::MAX_CTAS ? sm100_count() : decode::MAX_CTAS;
   const unsigned ctas = (unsigned)(most < sms ? most : sms);
-  const int workers = decode::workers_of(M);
-  attend<<<ctas, 32 * decode::warps_of(M), C::smem(M), s>>>(tk, tv, a, shape, static_cast<const T *>(q), sink, work, wait_limit());
+  attend<<<ctas, 32 * decode::warps_of(M), C::smem(M), s>>>(tk, tv, a, shape, static_cast<const T *>(q), sink, work,
+                                                          wait_limit());
   STA_CUDA_TRY(cudaGetLastError());
-  // Each kernel may start up while the one before it runs; it waits for that
-  // one's end before it reads anything.
+  // Each of the others may start up while the kernel before it runs; it waits
+  // for that one's end before it reads anything.
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas * workers);
+  // the fewer the rows, the fewer of their outputs to a CTA and the more
+  // threads to each
+  const long long rows = (long long)c->B * c->kv_heads, elements = (long long)M * D / 4;
+  int wide = 2;
+  while (wide < decode::JOIN_THREADS && wide < elements && rows * ((elements + wide - 1) / wide) > 8 * sms) wide *= 2;
+  cfg.gridDim = dim3((unsigned)rows, (unsigned)((elements + wide - 1) / wide));
   cfg.blockDim = dim3(decode::JOIN_THREADS);
   cfg.stream = s;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
   STA_CUDA_TRY(cudaLaunchKernelEx(&cfg, decode::join_kernel<D, T>, a, shape,
                                   static_cast<const decode::Sink<D, T>>(sink),
-                                  static_cast<const decode::Work>(work)));
+                                  static_cast<const decode::Work>(work), wide));
   if (MASS) {
     const long long pages = (most + decode::WEIGH_PAGES - 1) / decode::WEIGH_PAGES;
     cfg.gridDim = dim3((unsigned)(pages < 8 * sms ? pages : 8 * sms));  // at most what an SM holds

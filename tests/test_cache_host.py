@@ -2,8 +2,9 @@
 anything runs, workspace sizes, the binding's checks, and the oracle pinned
 to dense attention and to cases worked by hand."""
 import ctypes
-import runpy
 import os
+import runpy
+import subprocess
 
 import numpy as np
 import pytest
@@ -143,6 +144,69 @@ def test_the_description_of_a_cache_is_laid_out_as_in_the_header(sta):
                                                         "k_pages", "v_pages", "page_table", "lens", "seen",
                                                         "slot_pos", "weight"]
     assert ctypes.sizeof(sta.KvCacheDesc) == 6 * 4 + 7 * 8
+
+
+# -------------------------------------------------------- index arithmetic
+@pytest.fixture(scope="module")
+def index(tmp_path_factory):
+    """The kernels' index header, compiled for the host."""
+    d = tmp_path_factory.mktemp("index")
+    header = os.path.join(ROOT, "block_sparse_attention_28_b200", "csrc", "sta_cache_index.h")
+    (d / "index.cpp").write_text(f'''#include "{header}"
+using namespace sta::cache;
+extern "C" {{
+int length(int len, int max_pages) {{ return length_ok(len, max_pages); }}
+int page(int page, int num_pages) {{ return page_ok(page, num_pages); }}
+int filled(int len) {{ return filled_pages(len); }}
+int list(int first, int next, long long capacity, int max_pages) {{ return list_ok(first, next, capacity, max_pages); }}
+int column(int column, int before, int filled) {{ return column_ok(column, before, filled); }}
+int units(int pages) {{ return row_units(pages); }}
+// 0 if the chunks of `units` cover them one after another, none twice, in at
+// most `workers` chunks, and of() finds each unit in its chunk (of every unit,
+// or of the first and last of each chunk)
+int chunks(int units, int workers, int every) {{
+  const Chunks c = make_chunks(units, workers);
+  if (c.begin(0) != 0 || c.size < 1 || c.begin(workers) != units || c.begin(workers + 5) != units) return 1;
+  for (int i = 0; i < workers && c.begin(i) < units; ++i) {{
+    const int u0 = c.begin(i), u1 = c.begin(i + 1);
+    if (u0 >= u1 || c.of(u0) != i || c.of(u1 - 1) != i) return 2;
+    for (int u = u0; every && u < u1; ++u)
+      if (c.of(u) != i) return 3;
+  }}
+  return 0;
+}}
+int part(int chunk, int begins) {{ return part_of(chunk, begins != 0); }}
+}}''')
+    so = d / "index.so"
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-o", str(so), str(d / "index.cpp")], check=True)
+    lib = ctypes.CDLL(str(so))
+    lib.list.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_longlong, ctypes.c_int]
+    return lib
+
+
+def test_what_is_out_of_bounds(index):
+    """Lengths, page numbers, list offsets and entries that a kernel leaves out."""
+    top = 2**31 - 1
+    assert [index.length(n, 3) for n in (-2**31, -1, 0, 1, 192, 193, top)] == [0, 0, 1, 1, 1, 0, 0]
+    assert index.length(1 << 30, 1 << 24) and not index.length((1 << 30) + 1, 1 << 24)
+    assert [index.page(n, 7) for n in (-2**31, -1, 0, 6, 7, top)] == [0, 0, 1, 1, 0, 0]
+    assert [index.filled(n) for n in (-5, 0, 1, 64, 65, 1 << 30)] == [0, 0, 1, 1, 2, 1 << 24]
+    assert index.list(0, 0, 0, 1) and index.list(2, 6, 6, 4)
+    for bad in ((-1, 2, 9, 9), (3, 2, 9, 9), (2, 10, 9, 9), (0, 5, 9, 4), (-2**31, top, 9, 9), (top, -2**31, 9, 9)):
+        assert not index.list(*bad), bad
+    assert index.column(0, -1, 1) and index.column(5, 3, 6)
+    for bad in ((-1, -1, 4), (4, 3, 4), (2, 2, 4), (1, 2, 4), (0, -1, 0)):
+        assert not index.column(*bad), bad
+
+
+def test_chunks_cover_the_units_once(index):
+    for workers in (1, 2, 7, 32, 296, 592, 1036):
+        for units in list(range(0, 60)) + [workers * k + r for k in (1, 3, 4, 5, 13, 20, 100) for r in (-1, 0, 1)]:
+            assert index.chunks(units, workers, 1) == 0, (units, workers)
+        for units in (2**31 - 1, 2**31 - 2, 10**9 + 7):
+            assert index.chunks(units, workers, 0) == 0, (units, workers)
+    assert len({index.part(c, b) for c in range(9) for b in (0, 1)}) == 18
+    assert [index.units(n) for n in (0, 1, 5)] == [0, 2, 6]
 
 
 # ------------------------------------------------------------------- oracle

@@ -288,21 +288,34 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
   for (int c = 0; c < rank; ++c) pass_over(*cluster.map_shared_rank(&whole, c));
   for (int w = 0; w < warp; ++w) pass_over(tally[w]);
   const unsigned below_lane = (1u << lane) - 1u;
+  const bool no_ties = tally[warp].ties() == 0;
+  int *hole_list = holes + (long long)r * cap, *fill_list = fills + (long long)r * cap;
+#pragma unroll 2
   for (int j0 = lo; j0 < hi; j0 += 32) {
     const int j = j0 + lane;
     const bool in = j < hi;
     const unsigned k = in ? key_of(j) : 0u;
-    const bool equal = in && k == threshold;
-    const unsigned eq = __ballot_sync(0xFFFFFFFFu, equal);
-    const bool keep = in && (k > threshold || (equal && tie + __popc(eq & below_lane) < left));
-    const unsigned hm = __ballot_sync(0xFFFFFFFFu, in && !keep && j < edge);
-    const unsigned fm = __ballot_sync(0xFFFFFFFFu, keep && j >= edge);
-    const int at_hole = hole + __popc(hm & below_lane), at_fill = fill + __popc(fm & below_lane);
-    if ((hm >> lane & 1u) && at_hole < cap) holes[(long long)r * cap + at_hole] = begin + j;
-    if ((fm >> lane & 1u) && at_fill < cap) fills[(long long)r * cap + at_fill] = begin + j;
-    tie += __popc(eq);
-    hole += __popc(hm);
-    fill += __popc(fm);
+    bool keep = in && k > threshold;
+    if (!no_ties) {
+      const bool equal = in && k == threshold;
+      const unsigned eq = __ballot_sync(0xFFFFFFFFu, equal);
+      keep |= equal && tie + __popc(eq & below_lane) < left;
+      tie += __popc(eq);
+    }
+    if (j0 < edge) {
+      const bool is = in && !keep && j < edge;
+      const unsigned mask = __ballot_sync(0xFFFFFFFFu, is);
+      const int at = hole + __popc(mask & below_lane);
+      if (is && at < cap) hole_list[at] = begin + j;
+      hole += __popc(mask);
+    }
+    if (j0 + 32 > edge) {
+      const bool is = keep && j >= edge;
+      const unsigned mask = __ballot_sync(0xFFFFFFFFu, is);
+      const int at = fill + __popc(mask & below_lane);
+      if (is && at < cap) fill_list[at] = begin + j;
+      fill += __popc(mask);
+    }
   }
   if (rank == ranks - 1 && warp == W - 1 && lane == 0) {
     // as many holes as fills: `budget` slots stay in all (and never more than
@@ -318,42 +331,51 @@ constexpr int MOVE_UNROLL = 4;
 // Pairs (fill, hole) one CTA of move_kernel<D> takes per pass.
 template <int D>
 __host__ __device__ constexpr int move_pairs() {
-  return MOVE_THREADS / (D / 8) * MOVE_UNROLL;
+  return MOVE_THREADS / (D / 8) * MOVE_UNROLL;  // at most MOVE_THREADS
 }
 
-// grid.x = row, grid.y strides over its pairs; D/8 threads move one pair's key
-// and value, MOVE_UNROLL pairs in flight each, the first of them the position
-// and the weight. Sources and destinations are disjoint.
+// grid.x = row, grid.y strides over its pairs: a thread each moves position and
+// weight, D/8 threads key and value, MOVE_UNROLL pairs in flight. Sources and
+// destinations are disjoint.
 template <int D>
 __global__ void __launch_bounds__(MOVE_THREADS)
 move_kernel(Args a, int cap, const int *holes, const int *fills, const int *count) {
   constexpr int CPR = D / 8;
-  constexpr int GROUPS = MOVE_THREADS / CPR;
+  constexpr int GROUPS = MOVE_THREADS / CPR, PAIRS = move_pairs<D>();
   const int r = blockIdx.x, b = r / a.H, h = r - b * a.H;
   const int chunk = threadIdx.x % CPR, group = threadIdx.x / CPR;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = count[r];
-  for (int i0 = (int)blockIdx.y * move_pairs<D>(); i0 < n; i0 += (int)gridDim.y * move_pairs<D>()) {
+  const int *to_list = holes + (long long)r * cap, *of_list = fills + (long long)r * cap;
+  for (int i0 = (int)blockIdx.y * PAIRS; i0 < n; i0 += (int)gridDim.y * PAIRS) {
     uint4 k[MOVE_UNROLL], v[MOVE_UNROLL];
     long long dst[MOVE_UNROLL];
+    int to = -1, p = 0;
+    float w = 0.0f;
+    if ((int)threadIdx.x < PAIRS && i0 + (int)threadIdx.x < n) {
+      to = to_list[i0 + threadIdx.x];
+      const long long of = a.slot(r, of_list[i0 + threadIdx.x]);
+      p = a.pos[of];
+      w = a.weight[of];
+    }
 #pragma unroll
     for (int u = 0; u < MOVE_UNROLL; ++u) {
       const int i = i0 + u * GROUPS + group;
       dst[u] = -1;
       if (i < n) {
-        const int to = holes[(long long)r * cap + i], of = fills[(long long)r * cap + i];
-        const int pt = a.page(b, to), pf = a.page(b, of);
+        const int into = to_list[i], from = of_list[i];
+        const int pt = a.page(b, into), pf = a.page(b, from);
         if (pt >= 0 && pf >= 0) {
-          const long long src = a.row(pf, h, of) * CPR + chunk;
-          dst[u] = a.row(pt, h, to) * CPR + chunk;
+          const long long src = a.row(pf, h, from) * CPR + chunk;
+          dst[u] = a.row(pt, h, into) * CPR + chunk;
           k[u] = a.k[src];
           v[u] = a.v[src];
         }
-        if (chunk == 0) {
-          a.pos[a.slot(r, to)] = a.pos[a.slot(r, of)];
-          a.weight[a.slot(r, to)] = a.weight[a.slot(r, of)];
-        }
       }
+    }
+    if (to >= 0) {
+      a.pos[a.slot(r, to)] = p;
+      a.weight[a.slot(r, to)] = w;
     }
 #pragma unroll
     for (int u = 0; u < MOVE_UNROLL; ++u)

@@ -579,17 +579,19 @@ EvictWs evict_ws_layout(const sta_kv_cache *c, int32_t budget) {
   return w;
 }
 
-// One CTA per row, or a cluster of up to 8 for long rows: as long as a CTA has
-// more than 8192 slots and the GPU (two of the large CTAs per SM) has room, or
-// the keys do not fit in its shared memory.
+// One CTA per row, or a cluster for long rows: of up to 8 CTAs as long as each
+// has 8192 slots and an SM to itself (40 rows of 75,600 slots: 3 CTAs each take
+// 149 us with the moves, 4, some of them two to an SM, 183), and as many as the
+// keys need to fit in shared memory.
 template <int THREADS>
 sta_status launch_plan(const sta_kv_cache *c, const cache::Args &a, int budget, int recent, int sinks, int cap,
                        int *holes, int *fills, int *count, cudaStream_t s) {
   const long long rows = (long long)c->B * c->kv_heads, slots = (long long)cache::PAGE * c->max_pages;
-  int ranks = 1;
-  while (ranks < 8 && slots / ranks > 8192 &&
-         (rows * ranks * 2 <= 2 * decode::MAX_CTAS || slots / ranks > cache::PLAN_MAX_KEYS))
-    ranks *= 2;
+  const long long fit = decode::MAX_CTAS / rows, want = slots / 8192;
+  const long long need = (slots + cache::PLAN_MAX_KEYS - 1) / cache::PLAN_MAX_KEYS;
+  long long ranks = fit < want ? fit : want;
+  ranks = ranks > need ? ranks : need;
+  ranks = ranks < 1 ? 1 : (ranks > 8 ? 8 : ranks);
   if (rows * ranks >= (1LL << 31)) return STA_ERR_UNSUPPORTED;
   const long long share = (slots / ranks + 63) / 32 * 32;
   const int room = (int)(share < cache::PLAN_MAX_KEYS ? share : cache::PLAN_MAX_KEYS);
@@ -975,7 +977,7 @@ sta_status sta_cache_evict(const sta_kv_cache *cache, int32_t budget, int32_t re
   int *holes = reinterpret_cast<int *>(ws + w.holes), *fills = reinterpret_cast<int *>(ws + w.fills);
   int *count = reinterpret_cast<int *>(ws + w.count);
   sta_status run = cache::PAGE * cache->max_pages <= 4096
-                       ? launch_plan<256>(cache, a, budget, recent, sinks, w.cap, holes, fills, count, s)
+                       ? launch_plan<512>(cache, a, budget, recent, sinks, w.cap, holes, fills, count, s)
                        : launch_plan<1024>(cache, a, budget, recent, sinks, w.cap, holes, fills, count, s);
   if (run != STA_OK) return run;
   return cache->d == 128 ? launch_move<128>(cache, a, w.cap, holes, fills, count, s)

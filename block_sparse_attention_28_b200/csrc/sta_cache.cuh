@@ -36,10 +36,14 @@ struct Args {
   }
   // row (key or value of one token and head) of the pools
   __device__ __forceinline__ long long row(int page, int h, int j) const {
+    dbg_ok(page >= 0 && page < num_pages && h >= 0 && h < H && j >= 0);
     return ((long long)page * H + h) * PAGE + j % PAGE;
   }
   // index of slot j of row r in slot_pos and weight
-  __device__ __forceinline__ long long slot(int r, int j) const { return (long long)r * PAGE * max_pages + j; }
+  __device__ __forceinline__ long long slot(int r, int j) const {
+    dbg_ok(r >= 0 && r < B * H && j >= 0 && j < PAGE * max_pages);
+    return (long long)r * PAGE * max_pages + j;
+  }
 };
 
 // ------------------------------------------------------------------- append

@@ -150,6 +150,37 @@ __device__ __forceinline__ uint32_t transpose(uint32_t v) {
   return r;
 }
 
+// Bounded wait, as tc::mbar_wait. A thread that try_wait has suspended is not
+// woken by a short limit (on a B200 not within the 5 us of the longest wait
+// here, whatever the hint), so under a limit of less than some milliseconds the
+// barrier is polled.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile uint32_t *abort, long long limit) {
+  const bool sleep = limit >= 4LL * STA_WAIT_SLEEP_NS;
+  auto done = [&]() {
+    if (sleep) return tc::mbar_try_wait_sleep(bar, parity, STA_WAIT_SLEEP_NS);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0u;
+  };
+  if (done()) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (done()) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > limit) {
+      *abort = 1u;
+      record_error(DEV_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
 // ------------------------------------------------------------------- rows
 struct RowPages {
   int len, n, first;  // length, pages attended to, first entry of its list
@@ -275,13 +306,14 @@ struct Producer {
       int flags = none ? (SKIP | END) : w_flags;
       if (upper) flags = (flags & ~FIRST) | UPPER;
       if (!last) flags &= ~(LAST | END);
-      if (issued < stages || tc::mbar_wait(&empty[stage], ((issued / stages) & 1) ^ 1, abort, limit)) {
+      if (issued < stages || wait(&empty[stage], ((issued / stages) & 1) ^ 1, abort, limit)) {
         piece[stage] = Piece{w_row, w_unit, w_held - upper * KEYS, flags};
         if (flags & SKIP) {
           tc::mbar_arrive(&full[stage]);
         } else {
           const uint32_t dst = tc::smem_u32(ring + stage * C::STAGE_BYTES);
           const int y = w_y + upper * KEYS;
+          dbg_ok(y >= 0 && y <= (a.num_pages * a.H - 1) * PAGE + KEYS && (y & (KEYS - 1)) == 0);
           tc::mbar_expect_tx(&full[stage], C::STAGE_BYTES);
 #pragma unroll
           for (int e = 0; e < D / 64; ++e) tc::tma_load_2d(dst + e * HALF_BYTES, &tk, &full[stage], 64 * e, y);
@@ -650,7 +682,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
     __syncwarp();
     Piece d = p.piece[stage];
     if (mt == 0 && (d.flags & FIRST)) load_queries<D, NT, T>(q, a, s, d.row, m0, qb);
-    ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&p.full[stage], parity, &abort, limit));
+    ok = __all_sync(0xFFFFFFFFu, wait(&p.full[stage], parity, &abort, limit));
     if (!ok) break;
     if (mt != 0) {
       d = p.piece[stage];
@@ -665,6 +697,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
         for (int y = 0; y < 2; ++y) lim[n][y] = d.held - back[n][y];
       const uint32_t at = ring + stage * C::STAGE_BYTES;
       float *sc = nullptr;
+      if (MASS) dbg_ok(d.unit >= 0 && d.unit < chunks.units && d.row >= 0 && d.row < rows);
       if (MASS) sc = work.scores + ((long long)d.unit * M + m0) * PAGE + (d.flags & UPPER ? KEYS : 0);
       if (d.held - (s.n_q - 1) < KEYS)
         attend_slots<D, NT, T, MASS, true>(at, lanes, qb, s, lim, d.held, acc, sc, tile_rows);

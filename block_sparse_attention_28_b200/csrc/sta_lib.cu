@@ -926,7 +926,7 @@ sta_status sta_attn_fwd_cached(const sta_kv_cache *cache, const void *q, void *o
   sta_status st = cache_args(cache, &a);
   if (st == STA_OK) st = decode_sizes(cache, q_heads, n_q, &group);
   if (st != STA_OK) return st;
-  if (q == nullptr || o == nullptr || !aligned16(q) || !aligned16(o) || !aligned4(lse) || !aligned4(page_ptr) ||
+  if (q == nullptr || o == nullptr || q == o || !aligned16(q) || !aligned16(o) || !aligned4(lse) || !aligned4(page_ptr) ||
       !aligned4(page_idx))
     return STA_ERR_INVALID_ARG;
   if ((page_ptr == nullptr) != (page_idx == nullptr) || idx_capacity < 0 ||

@@ -417,8 +417,9 @@ sta_status sta_cache_append(const sta_kv_cache *cache, const void *k_new, const 
 
 /* sta_attn_fwd_cached -- attention of a sequence's newest tokens over its
  * cache (block-sparse when page lists are given).
- *   q, o    : [B, n_q, q_heads, d]; the n_q newest tokens of each sequence,
- *             already appended; q head j reads key head j / (q_heads / kv_heads)
+ *   q, o    : [B, n_q, q_heads, d], not overlapping; the n_q newest tokens of
+ *             each sequence, already appended; q head j reads key head
+ *             j / (q_heads / kv_heads)
  *   lse     : optional fp32 [B, q_heads, n_q] (natural log); NULL to skip
  *   page_ptr: optional device int32 [B*kv_heads + 1], page_idx int32
  *             [idx_capacity]: CSR over rows b*kv_heads + h of the page columns

@@ -44,7 +44,7 @@ def calls(sta, d, ws=256, ws_bytes=1 << 30):
     lib = sta._lib
     return {
         "append": lib.sta_cache_append(p, 16, 16, 3, None, None),
-        "attend": lib.sta_attn_fwd_cached(p, 16, 16, None, 8, 1, None, None, 0, 0, ws, ws_bytes, 0.0, None),
+        "attend": lib.sta_attn_fwd_cached(p, 16, 32, None, 8, 1, None, None, 0, 0, ws, ws_bytes, 0.0, None),
         "evict": lib.sta_cache_evict(p, 16, 4, 2, ws, ws_bytes, None),
     }
 
@@ -68,11 +68,11 @@ def test_bad_arguments_are_refused(sta):
                                   (16, 16, 1 << 22, None, UNS)):
         assert lib.sta_cache_append(p, k, v, n, counts, None) == want
 
-    def attend(q=16, o=16, lse=None, heads=8, n_q=1, ptr=None, idx=None, cap=0, acc=0, ws=256, n=1 << 30, scale=0.0,
+    def attend(q=16, o=32, lse=None, heads=8, n_q=1, ptr=None, idx=None, cap=0, acc=0, ws=256, n=1 << 30, scale=0.0,
                c=good):
         return lib.sta_attn_fwd_cached(ctypes.byref(c), q, o, lse, heads, n_q, ptr, idx, cap, acc, ws, n, scale, None)
 
-    for kw, want in ((dict(q=None), INV), (dict(o=None), INV), (dict(q=8), INV), (dict(o=24), INV), (dict(lse=2), INV),
+    for kw, want in ((dict(q=None), INV), (dict(o=None), INV), (dict(o=16), INV), (dict(q=8), INV), (dict(o=24), INV), (dict(lse=2), INV),
                      (dict(heads=0), INV), (dict(heads=6), INV), (dict(n_q=0), INV), (dict(heads=8, n_q=33), UNS),
                      (dict(heads=4 * 65), UNS), (dict(ptr=16), INV), (dict(idx=16), INV), (dict(cap=4), INV),
                      (dict(ptr=16, idx=16, cap=-1), INV), (dict(ptr=17, idx=16, cap=4), INV), (dict(acc=2), INV),

@@ -258,6 +258,71 @@ def test_non_finite_values_of_a_newer_token(sta):
         C.check_attention(o[:, :2], lse[:, :, :2], early, 64, "bf16", 130)
 
 
+@pytest.mark.parametrize("d,group,n_q,kv", [(64, 1, 4, 2), (128, 5, 3, 1), (128, 4, 6, 1), (64, 8, 8, 1),
+                                            (128, 1, 64, 1)])
+@pytest.mark.parametrize("what", ["k_pages", "v_pages"])
+def test_non_finite_draft_tokens(sta, d, group, n_q, kv, what):
+    """Every second one of the newest tokens has a key or a value that is not
+    finite: a query is touched by those it sees and by no others, whatever
+    page and piece of a page they lie in."""
+    lens = [n_q, 33, 64, 65, 70, 96, 127, 200]
+    t = C.make(lens, kv, d, "bf16", seed=50 + n_q)
+    q = C.queries(len(lens), n_q, kv * group, d, "bf16", seed=51)
+    for b, n in enumerate(lens):
+        for i in range(1, n_q, 2):
+            j = n - n_q + i
+            if j >= 0:
+                page = int(t["page_table"][b, j // C.PAGE])
+                t[what][page, :, j % C.PAGE, (7 * i) % d] = float("nan")
+    c = C.oracle(t)
+    o, lse = attend(sta, t, q)
+    ok(sta)
+    got = o.double().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        want, want_lse, sigma, terms = K.attend(c, q.double().cpu().numpy(), d ** -0.5)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    fine = torch.from_numpy(~np.isnan(want))
+    zero = lambda x: np.where(np.isnan(x), 0.0, x)  # noqa: E731
+    rows = ~np.isnan(want).any(-1)  # [B, n_q, heads]: nothing but finite outputs
+    C.check_attention(torch.where(fine & torch.from_numpy(rows)[..., None], o.cpu().float(), torch.tensor(0.0)), None,
+                      (zero(want) * rows[..., None], zero(want_lse), zero(sigma) * rows[..., None], zero(terms)), d,
+                      "bf16", 200)
+    if what == "k_pages":
+        assert np.array_equal(np.isnan(lse.cpu().numpy()), np.isnan(want_lse))
+
+
+def test_a_wait_that_runs_out_is_reported(sta):
+    """With a limit far below a load's latency (every SM fetching from a cache
+    four times the size of L2) waits give up: the call says so, ends, and the
+    next one is as ever."""
+    for d, group, n_q in ((128, 1, 1), (64, 8, 1), (128, 4, 5), (64, 8, 8)):
+        kv, B = 2, 8
+        pages = (256 << 20) // (kv * C.PAGE * d * 2)  # 256 MB of keys, as much of values
+        k, v = (torch.randn(pages, kv, C.PAGE, d, device="cuda").bfloat16() for _ in range(2))
+        width = pages // B
+        table = torch.randperm(pages, device="cuda")[:B * width].int().reshape(B, width).contiguous()
+        lens = torch.full((B, kv), C.PAGE * width - 5, dtype=torch.int32, device="cuda")
+        lens[3] = 0
+        t = {"k_pages": k, "v_pages": v, "page_table": table, "lens": lens, "seen": None, "slot_pos": None,
+             "weight": torch.zeros(B, kv, C.PAGE * width, device="cuda")}
+        q = C.queries(B, n_q, kv * group, d, "bf16", seed=61)
+        first = attend(sta, t, q, accumulate=True)
+        ok(sta)
+        weight = t["weight"].clone()
+        try:
+            sta.sta_set_wait_limit(1000)
+            attend(sta, t, q, accumulate=True)
+            torch.cuda.synchronize()
+            assert sta.sta_get_device_error() == sta.STA_ERR_TIMEOUT
+        finally:
+            sta.sta_set_wait_limit(0)
+        t["weight"].zero_()
+        again = attend(sta, t, q, accumulate=True)
+        ok(sta)
+        assert torch.equal(C.bits(first[0]), C.bits(again[0])) and torch.equal(first[1], again[1])
+        assert torch.equal(t["weight"], weight)
+
+
 def test_large_scores_and_a_given_scale(sta):
     """Scores of some hundreds: the maximum is taken off before the
     exponential; and one key far above the others."""
@@ -432,6 +497,7 @@ def test_evict_equal_weights_go_by_slot(sta):
     ([100_003, 64], 1, 20_000, 9000, 64, False),
     ([90_000], 3, 30_000, 0, 0, True),
     ([70_000], 200, 100, 10, 2, True),                # many rows: two CTAs, for the keys' sake
+    ([400_000], 1, 150_000, 1000, 64, True),          # more keys than a cluster's memory holds
 ])
 def test_evict_long_rows(sta, lens, kv, budget, recent, sinks, ties):
     """Rows shared out over a cluster of CTAs, with few equal weights and with

@@ -12,6 +12,12 @@
 namespace sta {
 namespace cache {
 
+// Start of every kernel of the cache calls: the next kernel of the stream may
+// start up beside this one, and this one goes on when the one before has ended
+// and its writes can be seen.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // sta_kv_cache as the kernels take it.
 struct Args {
   uint4 *k, *v;  // pages, in 16-byte chunks
@@ -58,6 +64,8 @@ __global__ void __launch_bounds__(APPEND_THREADS)
 append_kernel(Args a, const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new, int n_new,
               const int *__restrict__ counts) {
   constexpr unsigned CPR = D / 8;  // 16-byte chunks per row
+  let_next_start();
+  wait_for_previous();
   const int b = blockIdx.y;
   const int c = counts != nullptr ? counts[b] : n_new;
   if (c < 0 || c > n_new) {
@@ -163,7 +171,8 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int r = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_start();
+  wait_for_previous();
   const int len = a.length(r);
   if (len <= budget) {  // for the whole cluster alike
     if (tid == 0 && rank == 0) count[r] = 0;
@@ -348,7 +357,8 @@ move_kernel(Args a, int cap, const int *holes, const int *fills, const int *coun
   constexpr int GROUPS = MOVE_THREADS / CPR, PAIRS = move_pairs<D>();
   const int r = blockIdx.x, b = r / a.H, h = r - b * a.H;
   const int chunk = threadIdx.x % CPR, group = threadIdx.x / CPR;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  let_next_start();
+  wait_for_previous();
   const int n = count[r];
   const int *to_list = holes + (long long)r * cap, *of_list = fills + (long long)r * cap;
   for (int i0 = (int)blockIdx.y * PAIRS; i0 < n; i0 += (int)gridDim.y * PAIRS) {

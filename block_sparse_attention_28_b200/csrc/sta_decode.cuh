@@ -594,7 +594,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
   const int tiles = tiles_of(M), workers = workers_of(M), stages = C::stages(M);
   const int threads = blockDim.x;
   const int wk = warp / tiles, mt = warp % tiles, g = lane >> 2, t = lane & 3;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  cache::let_next_start();
   if (tid < workers * stages) {
     tc::mbar_init(&full[tid], 1);
     tc::mbar_init(&empty[tid], tiles);
@@ -605,6 +605,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
     asm volatile("prefetch.tensormap [%0];" ::"l"(&tk) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&tv) : "memory");
   }
+  cache::wait_for_previous();
   // units before each thread's rows; rows without pages get their zeros here
   const int per = (rows + threads - 1) / threads;
   const int lo = (int)min((long long)rows, (long long)tid * per), hi = min(rows, lo + per);
@@ -792,8 +793,8 @@ template <int D, typename T>
 __global__ void __launch_bounds__(JOIN_THREADS)
 join_kernel(const Args a, const Shape s, const Sink<D, T> sink, const Work work, int wide) {
   __shared__ Part parts[JOIN_THREADS];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  cache::let_next_start();
+  cache::wait_for_previous();
   const int tid = threadIdx.x, M = s.group * s.n_q;
   const cache::Chunks chunks = *work.chunks;
   const int r = blockIdx.x, first = work.row_units[r].x, n = work.row_units[r].y;
@@ -840,7 +841,8 @@ constexpr int WEIGH_PAGES = WEIGH_THREADS / PAGE;  // of a CTA at a time
 // A thread per slot; the grid strides over the pages.
 __global__ void __launch_bounds__(WEIGH_THREADS)
 weigh_kernel(const Args a, const int M, const Work work) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  cache::let_next_start();
+  cache::wait_for_previous();
   const int rows = a.B * a.H, units = work.chunks->units;
   const int j = threadIdx.x % PAGE, step = (int)gridDim.x * WEIGH_PAGES;
   int u = (int)blockIdx.x * WEIGH_PAGES + (int)threadIdx.x / PAGE;

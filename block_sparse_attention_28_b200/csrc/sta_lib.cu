@@ -462,6 +462,31 @@ sta_status decode_sizes(const sta_kv_cache *c, int32_t q_heads, int32_t n_q, int
   return STA_OK;
 }
 
+// Launches a kernel of the cache calls: it may start up while the kernel before
+// it in the stream still runs, and waits (griddepcontrol.wait) for that one's
+// end before it touches memory. Saves the launch latency between the calls of
+// a decoding step, all of which let the next kernel start early. ranks: CTAs of
+// a cluster (0: no clusters).
+template <typename... Params, typename... Values>
+sta_status launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, int ranks, cudaStream_t s,
+                        const Values &...values) {
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = (unsigned)ranks;
+  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attrs;
+  cfg.numAttrs = ranks > 0 ? 2 : 1;
+  STA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(values)...));
+  return STA_OK;
+}
+
 // Workspace of the attention over a cache: per chunk two parts of rows cut by
 // its borders and their description; with accumulation also, per page
 // read, its row and column and its scores, and each row's log-sum-exp.
@@ -518,35 +543,20 @@ sta_status launch_decode(const sta_kv_cache *c, const cache::Args &a, const deco
   const long long most = (long long)c->B * c->kv_heads * c->max_pages;
   const int sms = sm100_count() < decode::MAX_CTAS ? sm100_count() : decode::MAX_CTAS;
   const unsigned ctas = (unsigned)(most < sms ? most : sms);
-  attend<<<ctas, 32 * decode::warps_of(M), C::smem(M), s>>>(tk, tv, a, shape, static_cast<const T *>(q), sink, work,
-                                                          wait_limit());
-  STA_CUDA_TRY(cudaGetLastError());
-  // Each of the others may start up while the kernel before it runs; it waits
-  // for that one's end before it reads anything.
-  cudaLaunchAttribute early;
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
+  sta_status st = launch_early(attend, dim3(ctas), 32 * decode::warps_of(M), C::smem(M), 0, s, tk, tv, a, shape,
+                               static_cast<const T *>(q), sink, work, wait_limit());
+  if (st != STA_OK) return st;
   // the fewer the rows, the fewer of their outputs to a CTA and the more
   // threads to each
   const long long rows = (long long)c->B * c->kv_heads, elements = (long long)M * D / 4;
   int wide = 2;
   while (wide < decode::JOIN_THREADS && wide < elements && rows * ((elements + wide - 1) / wide) > 8 * sms) wide *= 2;
-  cfg.gridDim = dim3((unsigned)rows, (unsigned)((elements + wide - 1) / wide));
-  cfg.blockDim = dim3(decode::JOIN_THREADS);
-  cfg.stream = s;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  STA_CUDA_TRY(cudaLaunchKernelEx(&cfg, decode::join_kernel<D, T>, a, shape,
-                                  static_cast<const decode::Sink<D, T>>(sink),
-                                  static_cast<const decode::Work>(work), wide));
-  if (MASS) {
-    const long long pages = (most + decode::WEIGH_PAGES - 1) / decode::WEIGH_PAGES;
-    cfg.gridDim = dim3((unsigned)(pages < 8 * sms ? pages : 8 * sms));  // at most what an SM holds
-    cfg.blockDim = dim3(decode::WEIGH_THREADS);
-    STA_CUDA_TRY(cudaLaunchKernelEx(&cfg, decode::weigh_kernel, a, M, static_cast<const decode::Work>(work)));
-  }
-  return STA_OK;
+  st = launch_early(decode::join_kernel<D, T>, dim3((unsigned)rows, (unsigned)((elements + wide - 1) / wide)),
+                    decode::JOIN_THREADS, 0, 0, s, a, shape, sink, work, wide);
+  if (st != STA_OK || !MASS) return st;
+  const long long pages = (most + decode::WEIGH_PAGES - 1) / decode::WEIGH_PAGES;
+  const unsigned weigh_ctas = (unsigned)(pages < 8 * sms ? pages : 8 * sms);  // at most what the SMs hold
+  return launch_early(decode::weigh_kernel, dim3(weigh_ctas), decode::WEIGH_THREADS, 0, 0, s, a, M, work);
 }
 
 template <int D, typename T>
@@ -598,37 +608,17 @@ sta_status launch_plan(const sta_kv_cache *c, const cache::Args &a, int budget, 
   const size_t smem = ((size_t)cache::PLAN_PASSES * cache::PLAN_BINS + room) * sizeof(unsigned);
   STA_CUDA_TRY(cudaFuncSetAttribute(cache::evict_plan_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)smem));
-  cudaLaunchAttribute cluster;
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = (unsigned)ranks;
-  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * ranks));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = &cluster;
-  cfg.numAttrs = 1;
-  STA_CUDA_TRY(cudaLaunchKernelEx(&cfg, cache::evict_plan_kernel<THREADS>, a, budget, recent, sinks, cap, room, holes,
-                                  fills, count));
-  return STA_OK;
+  return launch_early(cache::evict_plan_kernel<THREADS>, dim3((unsigned)(rows * ranks)), THREADS, smem, (int)ranks, s,
+                      a, budget, recent, sinks, cap, room, holes, fills, count);
 }
 
 template <int D>
 sta_status launch_move(const sta_kv_cache *c, const cache::Args &a, int cap, const int *holes, const int *fills,
                        const int *count, cudaStream_t s) {
   const long long passes = ((long long)cap + cache::move_pairs<D>() - 1) / cache::move_pairs<D>();
-  cudaLaunchAttribute early;  // starts up while the plan is made, waits for its end
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(c->B * c->kv_heads), (unsigned)(passes < 65535 ? passes : 65535));
-  cfg.blockDim = dim3(cache::MOVE_THREADS);
-  cfg.stream = s;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  STA_CUDA_TRY(cudaLaunchKernelEx(&cfg, cache::move_kernel<D>, a, cap, holes, fills, count));
-  return STA_OK;
+  return launch_early(cache::move_kernel<D>,
+                      dim3((unsigned)(c->B * c->kv_heads), (unsigned)(passes < 65535 ? passes : 65535)),
+                      cache::MOVE_THREADS, 0, 0, s, a, cap, holes, fills, count);
 }
 
 }  // namespace
@@ -903,12 +893,9 @@ sta_status sta_cache_append(const sta_kv_cache *cache, const void *k_new, const 
   const long long per_cta = cache::APPEND_THREADS * cache::APPEND_UNROLL;
   const dim3 grid((unsigned)((chunks + per_cta - 1) / per_cta), (unsigned)cache->B);
   const uint4 *kn = static_cast<const uint4 *>(k_new), *vn = static_cast<const uint4 *>(v_new);
-  if (cache->d == 128)
-    cache::append_kernel<128><<<grid, cache::APPEND_THREADS, 0, s>>>(a, kn, vn, n_new, counts);
-  else
-    cache::append_kernel<64><<<grid, cache::APPEND_THREADS, 0, s>>>(a, kn, vn, n_new, counts);
-  STA_CUDA_TRY(cudaGetLastError());
-  return STA_OK;
+  return cache->d == 128
+             ? launch_early(cache::append_kernel<128>, grid, cache::APPEND_THREADS, 0, 0, s, a, kn, vn, n_new, counts)
+             : launch_early(cache::append_kernel<64>, grid, cache::APPEND_THREADS, 0, 0, s, a, kn, vn, n_new, counts);
 }
 
 size_t sta_attn_fwd_cached_workspace(const sta_kv_cache *cache, int32_t q_heads, int32_t n_q, int32_t accumulate) {

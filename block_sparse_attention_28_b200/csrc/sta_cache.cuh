@@ -173,12 +173,11 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
   const int r = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   let_next_start();
   wait_for_previous();
-  const int len = a.length(r);
+  const int len = a.length(r), from = a.seen[r] - recent;
   if (len <= budget) {  // for the whole cluster alike
     if (tid == 0 && rank == 0) count[r] = 0;
     return;
   }
-  const int from = a.seen[r] - recent;
   const int seg = ((len + ranks - 1) / ranks + 31) / 32 * 32;
   const int begin = min(len, rank * seg), n = min(len, begin + seg) - begin;
   const int *pos = a.pos + a.slot(r, begin);
@@ -240,8 +239,7 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
     const int upto = warp_scan(all);
     if (lane == 31) part[warp] = upto;
     __syncthreads();
-    int before = upto - all;
-    for (int w = 0; w < warp; ++w) before += part[w];
+    int before = upto - all + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? part[lane] : 0);
     if (before < left && left <= before + all) {
       int x = 0;
 #pragma unroll
@@ -299,7 +297,15 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
     tie += v.ties();
   };
   for (int c = 0; c < rank; ++c) pass_over(*cluster.map_shared_rank(&whole, c));
-  for (int w = 0; w < warp; ++w) pass_over(tally[w]);
+  {
+    Tally v = {0, 0, 0, 0};  // of warp `lane`, if it comes before this one
+    if (lane < warp) v = tally[lane];
+    const int upto = warp_scan(v.ties());
+    const int take = max(0, min(left - tie - (upto - v.ties()), v.ties()));
+    hole += __reduce_add_sync(0xFFFFFFFFu, v.holes(take));
+    fill += __reduce_add_sync(0xFFFFFFFFu, v.fills(take));
+    tie += __shfl_sync(0xFFFFFFFFu, upto, 31);
+  }
   const unsigned below_lane = (1u << lane) - 1u;
   const bool no_ties = tally[warp].ties() == 0;
   int *hole_list = holes + (long long)r * cap, *fill_list = fills + (long long)r * cap;

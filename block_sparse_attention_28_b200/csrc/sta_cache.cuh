@@ -26,8 +26,8 @@ struct Args {
   float *weight;
   int B, H, num_pages, max_pages;
   // length of row r = b*H + h, or -1 (recorded) if the page table cannot hold it
-  __device__ __forceinline__ int length(int r) const {
-    const int n = lens[r];
+  __device__ __forceinline__ int length(int r) const { return checked_length(lens[r]); }
+  __device__ __forceinline__ int checked_length(int n) const {
     if (length_ok(n, max_pages)) return n;
     record_error(DEV_ERR_BAD_CACHE);
     return -1;
@@ -145,19 +145,70 @@ struct Tally {
   __device__ __forceinline__ int ties() const { return tie_below + tie_above; }
 };
 
+// Moves the n pairs (fill, hole) of row r that one CTA of THREADS threads takes
+// at a time, from pair i0 on and then every `step`: a thread each moves position
+// and weight, D/8 threads key and value, UNROLL pairs in flight. Sources and
+// destinations are disjoint.
+template <int D, int THREADS, int UNROLL>
+__device__ __forceinline__ void move_pairs(const Args &a, int r, const int *holes, const int *fills, int n, int i0,
+                                           int step) {
+  constexpr int CPR = D / 8;
+  constexpr int GROUPS = THREADS / CPR, PAIRS = GROUPS * UNROLL;
+  static_assert(PAIRS <= THREADS, "a thread for every pair");
+  const int b = r / a.H, h = r - b * a.H;
+  const int chunk = threadIdx.x % CPR, group = threadIdx.x / CPR;
+  for (; i0 < n; i0 += step) {
+    uint4 k[UNROLL], v[UNROLL];
+    long long dst[UNROLL];
+    int to = -1, p = 0;
+    float w = 0.0f;
+    if ((int)threadIdx.x < PAIRS && i0 + (int)threadIdx.x < n) {
+      to = holes[i0 + threadIdx.x];
+      const long long of = a.slot(r, fills[i0 + threadIdx.x]);
+      p = a.pos[of];
+      w = a.weight[of];
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int i = i0 + u * GROUPS + group;
+      dst[u] = -1;
+      if (i < n) {
+        const int into = holes[i], from = fills[i];
+        const int pt = a.page(b, into), pf = a.page(b, from);
+        if (pt >= 0 && pf >= 0) {
+          const long long src = a.row(pf, h, from) * CPR + chunk;
+          dst[u] = a.row(pt, h, into) * CPR + chunk;
+          k[u] = a.k[src];
+          v[u] = a.v[src];
+        }
+      }
+    }
+    if (to >= 0) {
+      a.pos[a.slot(r, to)] = p;
+      a.weight[a.slot(r, to)] = w;
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u)
+      if (dst[u] >= 0) {
+        a.k[dst[u]] = k[u];
+        a.v[dst[u]] = v[u];
+      }
+  }
+}
+
 // A cluster of CTAs per (sequence, head), each with an equal range of the slots
 // and their keys in shared memory (read once; past key_room they are read
 // again). The budget-th largest key is found by radix selection on histograms
 // that every CTA sums up over the cluster; one more pass over the keys counts
 // ties, holes (slots given up below the budget) and fills (slots kept above
 // it) per warp, and a last one lists holes and fills, both in slot order.
-// holes, fills [rows, cap], count [rows]. The length is updated here, the rest
-// by move_kernel. The key reads (8 bytes per slot) are the floor; what bounds
+// holes, fills [rows, cap], count [rows]. The length is updated here; the rest
+// by move_kernel, or (D > 0, one CTA per row) here as well. The key reads (8 bytes per slot) are the floor; what bounds
 // it is latency: some ten steps that each wait for the one before.
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS)
-evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_room, int *__restrict__ holes,
-                  int *__restrict__ fills, int *__restrict__ count) {
+template <int THREADS, int D>
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1)
+evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_room, int *holes, int *fills,
+                  int *count) {
   constexpr int W = THREADS / 32;
   constexpr int PER = PLAN_BINS / THREADS;  // bins of a thread
   extern __shared__ unsigned plan_smem[];
@@ -175,7 +226,7 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
   wait_for_previous();
   const int len = a.length(r), from = a.seen[r] - recent;
   if (len <= budget) {  // for the whole cluster alike
-    if (tid == 0 && rank == 0) count[r] = 0;
+    if (D == 0 && tid == 0 && rank == 0) count[r] = 0;
     return;
   }
   const int seg = ((len + ranks - 1) / ranks + 31) / 32 * 32;
@@ -339,71 +390,38 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
   if (rank == ranks - 1 && warp == W - 1 && lane == 0) {
     // as many holes as fills: `budget` slots stay in all (and never more than
     // the lists hold)
-    count[r] = min(min(hole, fill), cap);
+    const int pairs = min(min(hole, fill), cap);
+    if (D > 0)
+      s_left = pairs;
+    else
+      count[r] = pairs;
     a.lens[r] = budget;
   }
   if (ranks > 1) cluster.sync();  // the others have read this CTA's memory
+  if constexpr (D > 0) {
+    __syncthreads();
+    constexpr int SHARE = THREADS / (D / 8) * 2;
+    move_pairs<D, THREADS, 2>(a, r, hole_list, fill_list, s_left, 0, SHARE);
+  }
 }
 
 constexpr int MOVE_THREADS = 256;
 constexpr int MOVE_UNROLL = 4;
-// Pairs (fill, hole) one CTA of move_kernel<D> takes per pass.
+// Pairs one CTA of move_kernel<D> takes at a time.
 template <int D>
-__host__ __device__ constexpr int move_pairs() {
-  return MOVE_THREADS / (D / 8) * MOVE_UNROLL;  // at most MOVE_THREADS
+__host__ __device__ constexpr int move_share() {
+  return MOVE_THREADS / (D / 8) * MOVE_UNROLL;
 }
 
-// grid.x = row, grid.y strides over its pairs: a thread each moves position and
-// weight, D/8 threads key and value, MOVE_UNROLL pairs in flight. Sources and
-// destinations are disjoint.
+// grid.x = row, grid.y strides over its pairs.
 template <int D>
 __global__ void __launch_bounds__(MOVE_THREADS)
 move_kernel(Args a, int cap, const int *holes, const int *fills, const int *count) {
-  constexpr int CPR = D / 8;
-  constexpr int GROUPS = MOVE_THREADS / CPR, PAIRS = move_pairs<D>();
-  const int r = blockIdx.x, b = r / a.H, h = r - b * a.H;
-  const int chunk = threadIdx.x % CPR, group = threadIdx.x / CPR;
   let_next_start();
   wait_for_previous();
-  const int n = count[r];
-  const int *to_list = holes + (long long)r * cap, *of_list = fills + (long long)r * cap;
-  for (int i0 = (int)blockIdx.y * PAIRS; i0 < n; i0 += (int)gridDim.y * PAIRS) {
-    uint4 k[MOVE_UNROLL], v[MOVE_UNROLL];
-    long long dst[MOVE_UNROLL];
-    int to = -1, p = 0;
-    float w = 0.0f;
-    if ((int)threadIdx.x < PAIRS && i0 + (int)threadIdx.x < n) {
-      to = to_list[i0 + threadIdx.x];
-      const long long of = a.slot(r, of_list[i0 + threadIdx.x]);
-      p = a.pos[of];
-      w = a.weight[of];
-    }
-#pragma unroll
-    for (int u = 0; u < MOVE_UNROLL; ++u) {
-      const int i = i0 + u * GROUPS + group;
-      dst[u] = -1;
-      if (i < n) {
-        const int into = to_list[i], from = of_list[i];
-        const int pt = a.page(b, into), pf = a.page(b, from);
-        if (pt >= 0 && pf >= 0) {
-          const long long src = a.row(pf, h, from) * CPR + chunk;
-          dst[u] = a.row(pt, h, into) * CPR + chunk;
-          k[u] = a.k[src];
-          v[u] = a.v[src];
-        }
-      }
-    }
-    if (to >= 0) {
-      a.pos[a.slot(r, to)] = p;
-      a.weight[a.slot(r, to)] = w;
-    }
-#pragma unroll
-    for (int u = 0; u < MOVE_UNROLL; ++u)
-      if (dst[u] >= 0) {
-        a.k[dst[u]] = k[u];
-        a.v[dst[u]] = v[u];
-      }
-  }
+  const int r = blockIdx.x;
+  move_pairs<D, MOVE_THREADS, MOVE_UNROLL>(a, r, holes + (long long)r * cap, fills + (long long)r * cap, count[r],
+                                           (int)blockIdx.y * move_share<D>(), (int)gridDim.y * move_share<D>());
 }
 
 }  // namespace cache

@@ -185,13 +185,13 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile ui
 struct RowPages {
   int len, n, first;  // length, pages attended to, first entry of its list
 };
-__device__ __forceinline__ RowPages row_pages(const Args &a, const Shape &s, int r) {
+// (first, next: the row's offsets, where there are lists)
+__device__ __forceinline__ RowPages row_pages(const Args &a, const Shape &s, int len, int first, int next) {
   RowPages p;
-  p.len = a.length(r);
+  p.len = a.checked_length(len);
   p.n = cache::filled_pages(p.len);
   p.first = 0;
   if (s.page_ptr != nullptr) {
-    const int first = s.page_ptr[r], next = s.page_ptr[r + 1];
     if (!cache::list_ok(first, next, s.idx_capacity, a.max_pages)) {
       record_error(DEV_ERR_BAD_MASK);
       p.n = 0;
@@ -201,6 +201,10 @@ __device__ __forceinline__ RowPages row_pages(const Args &a, const Shape &s, int
     }
   }
   return p;
+}
+__device__ __forceinline__ RowPages row_pages(const Args &a, const Shape &s, int r) {
+  const bool lists = s.page_ptr != nullptr;
+  return row_pages(a, s, a.lens[r], lists ? s.page_ptr[r] : 0, lists ? s.page_ptr[r + 1] : 0);
 }
 
 // --------------------------------------------------------------- producer
@@ -610,14 +614,29 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
   const int per = (rows + threads - 1) / threads;
   const int lo = (int)min((long long)rows, (long long)tid * per), hi = min(rows, lo + per);
   int mine = 0;
-  for (int r = lo; r < hi; ++r) {
-    const int n = row_pages(a, s, r).n;
-    mine += cache::row_units(n);
-    if (n == 0 && r % gridDim.x == blockIdx.x) {
-      sink.put_nothing(a, s, r);
-      work.row_units[r] = make_int2(0, 0);
-    }
+  bool none = false;
+  for (int r0 = lo; r0 < hi; r0 += 8) {
+    // eight rows' lengths and lists on their way at once
+    int len[8], ptr[9];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) len[x] = r0 + x < hi ? a.lens[r0 + x] : 0;
+    if (s.page_ptr != nullptr)
+#pragma unroll
+      for (int x = 0; x < 9; ++x) ptr[x] = r0 + x <= hi ? s.page_ptr[r0 + x] : 0;
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      if (r0 + x < hi) {
+        const int n = row_pages(a, s, len[x], ptr[x], ptr[x + 1]).n;
+        mine += cache::row_units(n);
+        none |= n == 0;
+      }
   }
+  if (none)
+    for (int r = lo; r < hi; ++r)
+      if (r % gridDim.x == blockIdx.x && row_pages(a, s, r).n == 0) {
+        sink.put_nothing(a, s, r);
+        work.row_units[r] = make_int2(0, 0);
+      }
   const int upto = cache::warp_scan(mine);
   if (lane == 31) warp_units[warp] = upto;
   __syncthreads();

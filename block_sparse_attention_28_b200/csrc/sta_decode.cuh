@@ -786,6 +786,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
 }
 
 constexpr int JOIN_THREADS = 128;
+constexpr int JOIN_BATCH = 4;
 
 // A part of a row's sum: the weights' maximum (log2) and sum, four outputs. A
 // sum of 0 is nothing.
@@ -823,11 +824,20 @@ join_kernel(const Args a, const Shape s, const Sink<D, T> sink, const Work work,
   const int e = (int)blockIdx.y * wide + tid % wide, m = e / (D / 4);
   Part sum = {0.0f, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
   if (m < M)
-#pragma unroll 4
-    for (int c = c0 + tid / wide; c <= c1; c += JOIN_THREADS / wide) {
-      const long long at = (long long)cache::part_of(c, c == c0) * M + m;
-      const float2 ml = work.part_ml[at];
-      sum.add(Part{ml.x, ml.y, *reinterpret_cast<const float4 *>(work.part_o + at * D + e % (D / 4) * 4)});
+    for (int c = c0 + tid / wide; c <= c1; c += JOIN_BATCH * (JOIN_THREADS / wide)) {
+      Part p[JOIN_BATCH];  // on their way at once
+#pragma unroll
+      for (int x = 0; x < JOIN_BATCH; ++x) {
+        const int cx = c + x * (JOIN_THREADS / wide);
+        p[x].sum = 0.0f;
+        if (cx <= c1) {
+          const long long at = (long long)cache::part_of(cx, cx == c0) * M + m;
+          const float2 ml = work.part_ml[at];
+          p[x] = Part{ml.x, ml.y, *reinterpret_cast<const float4 *>(work.part_o + at * D + e % (D / 4) * 4)};
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < JOIN_BATCH; ++x) sum.add(p[x]);
     }
   for (int d = wide; d < 32; d *= 2) {
     Part p;

@@ -787,6 +787,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
 
 constexpr int JOIN_THREADS = 128;
 constexpr int JOIN_BATCH = 4;
+constexpr int JOIN_SPREAD = 200 * 1024;
 
 // A part of a row's sum: the weights' maximum (log2) and sum, four outputs. A
 // sum of 0 is nothing.

@@ -374,8 +374,8 @@ class KVCache:
         its address (None: not given)."""
         if t is None and optional:
             return None
-        if t is None or t.dtype is not dtype or t.get_device() != self.index or not t.is_contiguous() or \
-                (shape is not None and t.shape != shape):
+        if t is None or t.dtype is not dtype or (shape is not None and t.shape != shape) or not t.is_contiguous() or \
+                t.get_device() != self.index:
             got = "None" if t is None else f"{t.dtype} {list(t.shape)} strides {list(t.stride())} on {t.device}"
             raise ValueError(f"{name}: contiguous {dtype} {'' if shape is None else list(shape)} on {self.device}, "
                              f"not {got}")
@@ -384,16 +384,22 @@ class KVCache:
     def _call(self, stream, fn, what, *args):
         """fn(description, *args, stream) with the cache's device current, on
         torch's current stream of that device unless one is given."""
-        if self.index < 0:
+        index = self.index
+        if index < 0:
             raise ValueError(f"{what}: the cache is on {self.device}, not on a GPU")
-        if self.index != torch.cuda.current_device():
-            with torch.cuda.device(self.index):
+        if index != _current_device():
+            with torch.cuda.device(index):
                 return self._call(stream, fn, what, *args)
-        # (the raw handle: torch.cuda.current_stream() makes an object, 3 us)
-        raw = torch._C._cuda_getCurrentRawStream(self.index) if stream is None else _stream(stream)
-        status = fn(self._ref, *args, raw)
+        status = fn(self._ref, *args, _raw_stream(index) if stream is None else _stream(stream))
         if status != STA_OK:
             raise StaError(status, what)
+
+
+# The bare lookups behind torch.cuda.current_device() and current_stream(): a
+# decoding step makes these calls for every layer, and the objects around them
+# cost as much as a launch (3 us).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def kv_cache(k_pages, v_pages, page_table, lens, seen=None, slot_pos=None, weight=None):
@@ -406,10 +412,10 @@ def sta_cache_append(cache, k_new, v_new, counts=None, stream=None):
     lens (and seen) already count them; counts (int32 [B]): the rows of a
     padded batch that are tokens."""
     n_new = k_new.shape[1] if k_new.dim() == 4 else 0
-    shape = (cache.B, n_new, cache.kv_heads, cache.d)
-    cache._call(stream, _lib.sta_cache_append, "sta_cache_append",
-                cache._tensor("k_new", k_new, cache.dtype, shape), cache._tensor("v_new", v_new, cache.dtype, shape),
-                n_new, cache._tensor("counts", counts, torch.int32, (cache.B,), True))
+    shape, tensor = (cache.B, n_new, cache.kv_heads, cache.d), cache._tensor
+    cache._call(stream, _lib.sta_cache_append, "sta_cache_append", tensor("k_new", k_new, cache.dtype, shape),
+                tensor("v_new", v_new, cache.dtype, shape), n_new,
+                None if counts is None else tensor("counts", counts, torch.int32, (cache.B,)))
 
 
 def sta_attn_fwd_cached_workspace(cache, q_heads, n_q=1, accumulate=False):
@@ -422,18 +428,19 @@ def sta_attn_fwd_cached(cache, q, o, lse, workspace, page_ptr=None, page_idx=Non
     over the listed pages of each key head (CSR page_ptr int32
     [B*kv_heads + 1], page_idx int32); accumulate adds each slot's attention
     to cache.weight. workspace: uint8, sta_attn_fwd_cached_workspace() bytes."""
-    _, n_q, q_heads, _ = shape = q.shape if q.dim() == 4 else (0, 0, 0, 0)
-    if shape[0] != cache.B or shape[3] != cache.d:
+    B, n_q, q_heads, d = shape = q.shape if q.dim() == 4 else (0, 0, 0, 0)
+    if B != cache.B or d != cache.d:
         raise ValueError(f"q: [{cache.B}, n_q, q_heads, {cache.d}], not {list(q.shape)}")
-    ptr = cache._tensor("page_ptr", page_ptr, torch.int32, (cache.B * cache.kv_heads + 1,), True)
-    idx = cache._tensor("page_idx", page_idx, torch.int32, None, True)
-    capacity = 0 if page_idx is None else page_idx.numel()
-    if capacity == 0 and page_idx is not None:
-        idx = ptr  # torch has no address for a tensor of no elements; none is read
-    cache._call(stream, _lib.sta_attn_fwd_cached, "sta_attn_fwd_cached",
-                cache._tensor("q", q, cache.dtype, shape), cache._tensor("o", o, cache.dtype, shape),
-                cache._tensor("lse", lse, torch.float32, (cache.B, q_heads, n_q), True), q_heads, n_q, ptr, idx,
-                capacity, 1 if accumulate else 0, cache._tensor("workspace", workspace, torch.uint8, None),
+    tensor, ptr, idx, capacity = cache._tensor, None, None, 0
+    if page_ptr is not None or page_idx is not None:
+        ptr = tensor("page_ptr", page_ptr, torch.int32, (B * cache.kv_heads + 1,))
+        idx, capacity = tensor("page_idx", page_idx, torch.int32, None), page_idx.numel()
+        if capacity == 0:
+            idx = ptr  # torch has no address for a tensor of no elements; none is read
+    cache._call(stream, _lib.sta_attn_fwd_cached, "sta_attn_fwd_cached", tensor("q", q, cache.dtype, shape),
+                tensor("o", o, cache.dtype, shape),
+                None if lse is None else tensor("lse", lse, torch.float32, (B, q_heads, n_q)), q_heads, n_q, ptr, idx,
+                capacity, 1 if accumulate else 0, tensor("workspace", workspace, torch.uint8, None),
                 workspace.numel(), sm_scale)
 
 

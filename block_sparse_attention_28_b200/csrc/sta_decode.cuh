@@ -20,10 +20,14 @@
 // chunk border leave their parts (the sum relative to a maximum) in the
 // workspace.
 // join_kernel: joins those parts.
+// Short rows (attend_kernel with CLUSTER): a cluster of CTAs per row, whose
+// workers share its pages and are joined through distributed shared memory; no
+// other kernel, and no part leaves the SMs.
 // weigh_kernel: adds every slot's attention to its weight now that the rows'
 // log-sum-exps are known, from the scores that attend_kernel left (4 bytes per
 // slot and query row against 4 d for its key and value).
 #pragma once
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
 #include "sta_cache.cuh"
@@ -42,6 +46,7 @@ constexpr int KEYS = 32;      // slots of a stage of the ring
 constexpr int KT = KEYS / 16;
 constexpr int HALF_BYTES = KEYS * 128;  // 64 values of every slot
 constexpr int MAX_STAGES = 28;          // of all workers
+constexpr int JOIN_BATCH = 4;
 constexpr long long DRAIN_LIMIT = 200000000LL;
 
 // Warps of a worker (16 query rows each) and workers of a CTA. Seven workers
@@ -280,7 +285,7 @@ struct Producer {
       if (w_unit == u1 - 1 || (i == n - 1 && w_unit == u1 - 2)) w_flags |= END;
       if (begins) w_flags |= BEGINS;
       if (begins && start + n <= u1) w_flags |= WHOLE;
-      if (i == 0) work.row_units[w_row] = make_int2(start, w_flags & WHOLE ? 0 : n);
+      if (i == 0 && work.row_units != nullptr) work.row_units[w_row] = make_int2(start, w_flags & WHOLE ? 0 : n);
     }
     if (work.units != nullptr && lane < take)
       work.units[w_unit] = col >= 0 ? make_int2(w_row, pack_page(col, w_held)) : make_int2(-1, -1);
@@ -582,7 +587,37 @@ struct Sink {
   }
 };
 
-template <int D, int NT, typename T, bool MASS>
+// A part of a row's sum: the weights' maximum (log2) and sum, four outputs. A
+// sum of 0 is nothing.
+struct Part {
+  float top, sum;
+  float4 o;
+  __device__ __forceinline__ void add(const Part &p) {
+    if (p.sum == 0.0f) return;
+    const float up = sum == 0.0f ? p.top : fmaxf(top, p.top);
+    const float x = sum == 0.0f ? 0.0f : tc::ex2(top - up), y = tc::ex2(p.top - up);
+    top = up;
+    sum = sum * x + p.sum * y;
+    o.x = o.x * x + p.o.x * y;
+    o.y = o.y * x + p.o.y * y;
+    o.z = o.z * x + p.o.z * y;
+    o.w = o.w * x + p.o.w * y;
+  }
+};
+
+__device__ __forceinline__ Part shuffled(const Part &v, int d) {
+  Part p;
+  p.top = __shfl_xor_sync(0xFFFFFFFFu, v.top, d);
+  p.sum = __shfl_xor_sync(0xFFFFFFFFu, v.sum, d);
+  p.o.x = __shfl_xor_sync(0xFFFFFFFFu, v.o.x, d);
+  p.o.y = __shfl_xor_sync(0xFFFFFFFFu, v.o.y, d);
+  p.o.z = __shfl_xor_sync(0xFFFFFFFFu, v.o.z, d);
+  p.o.w = __shfl_xor_sync(0xFFFFFFFFu, v.o.w, d);
+  return p;
+}
+
+// CLUSTER: grid.x = rows x CTAs of a cluster.
+template <int D, int NT, typename T, bool MASS, bool CLUSTER>
 __global__ void __launch_bounds__(32 * MAX_WARPS, 1)
 attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const Args a,
               const Shape s, const T *__restrict__ q, const Sink<D, T> sink, const Work work, long long limit) {
@@ -610,54 +645,75 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
     asm volatile("prefetch.tensormap [%0];" ::"l"(&tv) : "memory");
   }
   cache::wait_for_previous();
-  // units before each thread's rows; rows without pages get their zeros here
-  const int per = (rows + threads - 1) / threads;
-  const int lo = (int)min((long long)rows, (long long)tid * per), hi = min(rows, lo + per);
-  int mine = 0;
-  bool none = false;
-  for (int r0 = lo; r0 < hi; r0 += 8) {
-    // eight rows' lengths and lists on their way at once
-    int len[8], ptr[9];
-#pragma unroll
-    for (int x = 0; x < 8; ++x) len[x] = r0 + x < hi ? a.lens[r0 + x] : 0;
-    if (s.page_ptr != nullptr)
-#pragma unroll
-      for (int x = 0; x < 9; ++x) ptr[x] = r0 + x <= hi ? s.page_ptr[r0 + x] : 0;
-#pragma unroll
-    for (int x = 0; x < 8; ++x)
-      if (r0 + x < hi) {
-        const int n = row_pages(a, s, len[x], ptr[x], ptr[x + 1]).n;
-        mine += cache::row_units(n);
-        none |= n == 0;
-      }
-  }
-  if (none)
-    for (int r = lo; r < hi; ++r)
-      if (r % gridDim.x == blockIdx.x && row_pages(a, s, r).n == 0) {
-        sink.put_nothing(a, s, r);
-        work.row_units[r] = make_int2(0, 0);
-      }
-  const int upto = cache::warp_scan(mine);
-  if (lane == 31) warp_units[warp] = upto;
-  __syncthreads();
-  int units = 0, before = upto - mine;
-#pragma unroll
-  for (int w = 0; w < MAX_WARPS; ++w) {
-    if (32 * w >= threads) break;
-    if (w < warp) before += warp_units[w];
-    units += warp_units[w];
-  }
-  row_before[tid] = before;
-  __syncthreads();
-  const cache::Chunks chunks = cache::make_chunks(units, workers * gridDim.x);
-  if (tid == 0 && blockIdx.x == 0) *work.chunks = chunks;
-
-  // few units: a worker of every SM before a second one of any
-  const int worker = wk * gridDim.x + blockIdx.x;
+  namespace cg = cooperative_groups;
+  const int ranks = CLUSTER ? (int)cg::this_cluster().num_blocks() : 1;
+  const int rank = CLUSTER ? (int)cg::this_cluster().block_rank() : 0;
+  const int row = (int)blockIdx.x / ranks;  // CLUSTER: this CTA's
   Producer<D> p;
-  p.u = p.u0 = chunks.begin(worker);
-  p.u1 = chunks.begin(worker + 1);
-  if (p.u0 >= p.u1) return;
+  int worker, units = 0;
+  if constexpr (CLUSTER) {
+    // units are the row's own; its pages, shared out evenly
+    worker = wk * ranks + rank;
+    const int n = row_pages(a, s, row).n, all = workers * ranks;
+    p.u = p.u0 = cache::ROW_COST + (int)((long long)n * worker / all);
+    p.u1 = cache::ROW_COST + (int)((long long)n * (worker + 1) / all);
+    p.row = row;
+    p.off = p.u0;
+    units = p.u1;
+    __syncthreads();  // the barriers are there
+  } else {
+    // units before each thread's rows; rows without pages get their zeros here
+    const int per = (rows + threads - 1) / threads;
+    const int lo = (int)min((long long)rows, (long long)tid * per), hi = min(rows, lo + per);
+    int mine = 0;
+    bool none = false;
+    for (int r0 = lo; r0 < hi; r0 += 8) {
+      // eight rows' lengths and lists on their way at once
+      int len[8], ptr[9];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) len[x] = r0 + x < hi ? a.lens[r0 + x] : 0;
+      if (s.page_ptr != nullptr)
+#pragma unroll
+        for (int x = 0; x < 9; ++x) ptr[x] = r0 + x <= hi ? s.page_ptr[r0 + x] : 0;
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        if (r0 + x < hi) {
+          const int n = row_pages(a, s, len[x], ptr[x], ptr[x + 1]).n;
+          mine += cache::row_units(n);
+          none |= n == 0;
+        }
+    }
+    if (none)
+      for (int r = lo; r < hi; ++r)
+        if (r % gridDim.x == blockIdx.x && row_pages(a, s, r).n == 0) {
+          sink.put_nothing(a, s, r);
+          work.row_units[r] = make_int2(0, 0);
+        }
+    const int upto = cache::warp_scan(mine);
+    if (lane == 31) warp_units[warp] = upto;
+    __syncthreads();
+    int before = upto - mine;
+#pragma unroll
+    for (int w = 0; w < MAX_WARPS; ++w) {
+      if (32 * w >= threads) break;
+      if (w < warp) before += warp_units[w];
+      units += warp_units[w];
+    }
+    row_before[tid] = before;
+    __syncthreads();
+    const cache::Chunks chunks = cache::make_chunks(units, workers * gridDim.x);
+    if (tid == 0 && blockIdx.x == 0) *work.chunks = chunks;
+    worker = wk * gridDim.x + blockIdx.x;  // few units: a worker of every SM before a second one of any
+    p.u = p.u0 = chunks.begin(worker);
+    p.u1 = chunks.begin(worker + 1);
+    if (p.u0 >= p.u1) return;
+    if (mt == 0) {
+      int n = 0;  // threads whose rows begin at or before the chunk
+      for (int i = 0; i < threads; i += 32) n += __popc(__ballot_sync(0xFFFFFFFFu, row_before[i + lane] <= p.u0));
+      p.row = (n - 1) * per;
+      p.off = p.u0 - row_before[n - 1];
+    }
+  }
   p.ring = smem_raw + (1024 - (tc::smem_u32(smem_raw) & 1023u)) + wk * stages * C::STAGE_BYTES;
   p.full = full + wk * stages;
   p.empty = empty + wk * stages;
@@ -667,13 +723,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
   p.left = 0;
   p.ended = false;
   p.ok = true;
-  if (mt == 0) {
-    int n = 0;  // threads whose rows begin at or before the chunk
-    for (int i = 0; i < threads; i += 32) n += __popc(__ballot_sync(0xFFFFFFFFu, row_before[i + lane] <= p.u0));
-    p.row = (n - 1) * per;
-    p.off = p.u0 - row_before[n - 1];
-    p.find(a, s, rows, work);
-  }
+  if (mt == 0) p.find(a, s, rows, work);
   const int m0 = 16 * mt, tile_rows = min(8 * NT, M - m0);  // may be <= 0
   int back[NT][2];  // newer tokens than the query row's
 #pragma unroll
@@ -690,7 +740,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
   lanes.init<D>();
   const uint32_t ring = tc::smem_u32(p.ring);
   int stage = 0, parity = 0;
-  for (int it = 0;; ++it) {
+  if (CLUSTER) acc.clear();
+  for (int it = 0; !CLUSTER || p.u0 < p.u1; ++it) {
     if (mt == 0)
       while (p.ok && !p.ended && p.issued < it + stages) p.send(tk, tv, a, s, rows, work, &abort, limit);
     if (!p.ok) {
@@ -717,7 +768,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
         for (int y = 0; y < 2; ++y) lim[n][y] = d.held - back[n][y];
       const uint32_t at = ring + stage * C::STAGE_BYTES;
       float *sc = nullptr;
-      if (MASS) dbg_ok(d.unit >= 0 && d.unit < chunks.units && d.row >= 0 && d.row < rows);
+      if (MASS) dbg_ok(d.unit >= 0 && d.unit < units && d.row >= 0 && d.row < rows);
       if (MASS) sc = work.scores + ((long long)d.unit * M + m0) * PAGE + (d.flags & UPPER ? KEYS : 0);
       if (d.held - (s.n_q - 1) < KEYS)
         attend_slots<D, NT, T, MASS, true>(at, lanes, qb, s, lim, d.held, acc, sc, tile_rows);
@@ -730,7 +781,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
       stage = 0;
       parity ^= 1;
     }
-    if (d.flags & LAST) {
+    if (!CLUSTER && (d.flags & LAST)) {
       const long long part = (long long)cache::part_of(worker, d.flags & BEGINS) * M + m0;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -783,29 +834,72 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
   if (mt == 0 && lane == 0 && !(ok && p.ok))
     for (int x = max(0, p.issued - stages); x < p.issued; ++x)
       tc::mbar_wait(&p.full[x % stages], (x / stages) & 1, nullptr, DRAIN_LIMIT);
+  if constexpr (CLUSTER) {
+    // every worker's part into its own ring, which nobody reads from any more:
+    // outputs [M][D], then maximum and sum [M]
+    __syncthreads();
+    float *part_o = reinterpret_cast<float *>(p.ring);
+    float2 *part_ml = reinterpret_cast<float2 *>(part_o + M * D);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float sum = acc.sum[n][y];
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+        if (const int m = 8 * n + 2 * t + y; m < tile_rows) {
+          if (g == 0)
+            part_ml[m0 + m] = make_float2((acc.top[n][y] == -INFINITY ? 0.0f : acc.top[n][y]) - Num<T>::SHIFT, sum);
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) part_o[(m0 + m) * D + 16 * c + g + 8 * x] = acc.o[c][n][y + 2 * x];
+        }
+      }
+    cg::this_cluster().sync();
+    // The outputs, four to an element, are shared out among the CTAs; a warp
+    // has four elements at a time, and eight lanes for each that go through the
+    // CTAs' parts (ranks: 1, 2, 4 or 8).
+    const int elements = M * (D / 4), each = (elements + ranks - 1) / ranks;
+    const int e0 = rank * each, e1 = min(elements, e0 + each);
+    const int ring_floats = stages * C::STAGE_BYTES / 4, lane_parts = 8 / ranks;
+    const float *theirs = cg::this_cluster().map_shared_rank(
+        reinterpret_cast<float *>(p.ring - wk * stages * C::STAGE_BYTES), (lane / 4) & (ranks - 1));
+    const int first = (lane / 4) / ranks;  // of the workers of that CTA
+    for (int eb = e0 + 4 * warp; eb < e1; eb += 4 * (threads / 32)) {
+      const int e = min(eb + lane % 4, e1 - 1), m = e / (D / 4);
+      Part sum = {0.0f, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+      for (int k = first; k < workers; k += lane_parts * JOIN_BATCH) {
+        Part q[JOIN_BATCH];  // on their way at once
+#pragma unroll
+        for (int x = 0; x < JOIN_BATCH; ++x) {
+          const int w = k + lane_parts * x;
+          q[x].sum = 0.0f;
+          if (w < workers) {
+            const float *of = theirs + w * ring_floats;
+            const float2 ml = reinterpret_cast<const float2 *>(of + M * D)[m];
+            q[x] = Part{ml.x, ml.y, *reinterpret_cast<const float4 *>(of + e * 4)};
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < JOIN_BATCH; ++x) sum.add(q[x]);
+      }
+#pragma unroll
+      for (int d = 4; d < 32; d *= 2) sum.add(shuffled(sum, d));
+      if (lane < 4 && eb + lane < e1) {
+        const float z = sum.sum == 0.0f ? 0.0f : 1.0f / sum.sum;
+        *reinterpret_cast<uint2 *>(sink.o + sink.row(a, s, row, m) * D + e % (D / 4) * 4) =
+            make_uint2(Num<T>::pack(sum.o.x * z, sum.o.y * z), Num<T>::pack(sum.o.z * z, sum.o.w * z));
+        if (e % (D / 4) == 0) sink.put_lse(a, s, row, m, sum.sum == 0.0f ? -INFINITY : sum.top + log2f(sum.sum));
+      }
+    }
+    cg::this_cluster().sync();  // the others have read this CTA's memory
+  }
 }
 
 constexpr int JOIN_THREADS = 128;
-constexpr int JOIN_BATCH = 4;
 constexpr int JOIN_SPREAD = 200 * 1024;
-
-// A part of a row's sum: the weights' maximum (log2) and sum, four outputs. A
-// sum of 0 is nothing.
-struct Part {
-  float top, sum;
-  float4 o;
-  __device__ __forceinline__ void add(const Part &p) {
-    if (p.sum == 0.0f) return;
-    const float up = sum == 0.0f ? p.top : fmaxf(top, p.top);
-    const float x = sum == 0.0f ? 0.0f : tc::ex2(top - up), y = tc::ex2(p.top - up);
-    top = up;
-    sum = sum * x + p.sum * y;
-    o.x = o.x * x + p.o.x * y;
-    o.y = o.y * x + p.o.y * y;
-    o.z = o.z * x + p.o.z * y;
-    o.w = o.w * x + p.o.w * y;
-  }
-};
 
 // grid.x = rows; grid.y shares out a row's outputs, four to an element. Lanes
 // run along `wide` elements (a power of two), the rest of the CTA along the
@@ -840,16 +934,7 @@ join_kernel(const Args a, const Shape s, const Sink<D, T> sink, const Work work,
 #pragma unroll
       for (int x = 0; x < JOIN_BATCH; ++x) sum.add(p[x]);
     }
-  for (int d = wide; d < 32; d *= 2) {
-    Part p;
-    p.top = __shfl_xor_sync(0xFFFFFFFFu, sum.top, d);
-    p.sum = __shfl_xor_sync(0xFFFFFFFFu, sum.sum, d);
-    p.o.x = __shfl_xor_sync(0xFFFFFFFFu, sum.o.x, d);
-    p.o.y = __shfl_xor_sync(0xFFFFFFFFu, sum.o.y, d);
-    p.o.z = __shfl_xor_sync(0xFFFFFFFFu, sum.o.z, d);
-    p.o.w = __shfl_xor_sync(0xFFFFFFFFu, sum.o.w, d);
-    sum.add(p);
-  }
+  for (int d = wide; d < 32; d *= 2) sum.add(shuffled(sum, d));
   parts[tid] = sum;
   __syncthreads();
   if (tid >= wide || m >= M) return;

@@ -139,13 +139,16 @@ def test_append_leaves_out_what_does_not_fit(sta):
 LENGTHS = [0, 1, 2, 63, 64, 65, 127, 128, 129, 700]
 
 
+# columns of the page table: as many as the lengths need (few and short rows: a
+# cluster of CTAs each), or so many that the rows are shared out in chunks
+@pytest.mark.parametrize("max_pages", [None, 700])
 @pytest.mark.parametrize("d,dtype,kv,group,n_q", [
     (64, "bf16", 2, 1, 1), (128, "bf16", 1, 4, 1), (128, "fp16", 2, 8, 1), (64, "fp16", 1, 5, 3),
     (128, "bf16", 3, 1, 7), (64, "bf16", 1, 16, 4), (128, "fp16", 1, 1, 64), (128, "bf16", 2, 3, 9),
-    (128, "bf16", 1, 64, 1), (64, "fp16", 2, 17, 1),
+    (128, "bf16", 1, 64, 1), (64, "fp16", 2, 17, 1), (64, "bf16", 8, 1, 1), (128, "fp16", 12, 2, 1), (64, "fp16", 5, 2, 1),
 ])
-def test_attention_of_every_length(sta, d, dtype, kv, group, n_q):
-    t = C.make(LENGTHS, kv, d, dtype, seed=d + group + n_q)
+def test_attention_of_every_length(sta, d, dtype, kv, group, n_q, max_pages):
+    t = C.make(LENGTHS, kv, d, dtype, seed=d + group + n_q, max_pages=max_pages)
     q = C.queries(len(LENGTHS), n_q, kv * group, d, dtype, seed=3, scale=1.5)
     compare(sta, t, q, dtype)
 
@@ -157,7 +160,14 @@ def test_attention_of_every_length(sta, d, dtype, kv, group, n_q):
 def test_accumulated_weight(sta, d, dtype, kv, group, n_q):
     t = C.make(LENGTHS, kv, d, dtype, seed=d + group + n_q)
     q = C.queries(len(LENGTHS), n_q, kv * group, d, dtype, seed=4, scale=1.5)
-    o1, lse1 = compare(sta, t, q, dtype, accumulate=True)
+    compare(sta, t, q, dtype, accumulate=True)
+
+
+def test_accumulation_does_not_change_the_output(sta):
+    """Of rows shared out in chunks (short ones take other sums without it)."""
+    t = C.make(LENGTHS, 2, 128, "fp16", seed=138, max_pages=700)
+    q = C.queries(len(LENGTHS), 1, 16, 128, "fp16", seed=4, scale=1.5)
+    o1, lse1 = attend(sta, t, q, accumulate=True)
     o2, lse2 = attend(sta, t, q)
     ok(sta)
     assert torch.equal(C.bits(o1), C.bits(o2)) and torch.equal(lse1, lse2)
@@ -168,11 +178,11 @@ def test_heads_of_different_lengths(sta):
     compare(sta, t, C.queries(2, 2, 6, 128, "bf16", seed=5), "bf16", accumulate=True)
 
 
-@pytest.mark.parametrize("accumulate", [False, True])
-def test_page_lists(sta, accumulate):
+@pytest.mark.parametrize("accumulate,max_pages", [(False, None), (False, 700), (True, None)])
+def test_page_lists(sta, accumulate, max_pages):
     """Lists of some pages, of all, of none; the last page listed or not."""
     lens = [700, 700, 64, 0, 1000]
-    t = C.make(lens, 2, 128, "bf16", seed=6)
+    t = C.make(lens, 2, 128, "bf16", seed=6, max_pages=max_pages)
     lists = [[[0, 3, 10], []], [list(range(11)), [5]], [[0], []], [[], []], [[14, 15], [0, 1, 2, 7, 9, 13]]]
     q = C.queries(5, 3, 4, 128, "bf16", seed=6)
     compare(sta, t, q, "bf16", lists, accumulate)
@@ -185,7 +195,8 @@ def test_empty_lists_of_every_head(sta):
     assert (o == 0).all() and torch.isneginf(lse).all()
 
 
-def test_bad_list_entries_are_left_out(sta):
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_bad_list_entries_are_left_out(sta, accumulate):
     """The same index twice, one out of order, one past the last page, a
     negative one: recorded, the others attended to."""
     t = C.make([300, 300], 2, 64, "bf16", seed=8)
@@ -193,31 +204,33 @@ def test_bad_list_entries_are_left_out(sta):
     before = c["weight"].copy()
     q = C.queries(2, 1, 2, 64, "bf16", seed=8)
     given = [[[1, 1, 3], [2, 1, 4]], [[0, 5], [-1, 0]]]
-    o, lse = attend(sta, t, q, given, True)
+    o, lse = attend(sta, t, q, given, accumulate)
     torch.cuda.synchronize()
     assert sta.sta_get_device_error() == sta.STA_ERR_BAD_MASK
-    want = K.attend(c, q.double().cpu().numpy(), 64 ** -0.5, [[[1, 3], [2, 4]], [[0], [0]]], True)
+    want = K.attend(c, q.double().cpu().numpy(), 64 ** -0.5, [[[1, 3], [2, 4]], [[0], [0]]], accumulate)
     rel = C.check_attention(o, lse, want, 64, "bf16", 300)
     C.check_weight(t, c, before, rel, 1)
 
 
 @pytest.mark.parametrize("ptr", [[0, 2, 1, 3, 4], [0, 1, 2, 3, 99], [-3, 1, 2, 3, 4], [3, 2, 1, 0, -1]])
-def test_bad_list_offsets(sta, ptr):
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_bad_list_offsets(sta, ptr, accumulate):
     """Offsets that decrease, pass the entries or are negative: recorded, and
     nothing past the given entries is looked at; the outputs are finite."""
     t = C.make([300, 300], 2, 64, "bf16", seed=8)
     q = C.queries(2, 1, 2, 64, "bf16", seed=8)
     cache = cache_of(sta, t)
     o, lse = torch.zeros_like(q), torch.zeros(2, 2, 1, device="cuda")
-    ws = garbage(sta.sta_attn_fwd_cached_workspace(cache, 2, 1, True))
+    ws = garbage(sta.sta_attn_fwd_cached_workspace(cache, 2, 1, accumulate))
     sta.sta_attn_fwd_cached(cache, q, o, lse, ws, page_ptr=torch.tensor(ptr, dtype=torch.int32, device="cuda"),
-                            page_idx=torch.arange(4, dtype=torch.int32, device="cuda"), accumulate=True)
+                            page_idx=torch.arange(4, dtype=torch.int32, device="cuda"), accumulate=accumulate)
     torch.cuda.synchronize()
     assert sta.sta_get_device_error() == sta.STA_ERR_BAD_MASK
     assert torch.isfinite(o.float()).all() and torch.isfinite(t["weight"]).all()
 
 
-def test_bad_pages_and_lengths_are_left_out(sta):
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_bad_pages_and_lengths_are_left_out(sta, accumulate):
     t = C.make([200, 200, 200, 10], 1, 64, "bf16", seed=9)
     c = C.oracle(t)
     q = C.queries(4, 1, 1, 64, "bf16", seed=9)
@@ -227,10 +240,10 @@ def test_bad_pages_and_lengths_are_left_out(sta):
     t["lens"][2, 0] = 1 << 29
     c["lens"][2, 0] = c["lens"][3, 0] = 0
     before = c["weight"].copy()
-    o, lse = attend(sta, t, q, accumulate=True)
+    o, lse = attend(sta, t, q, accumulate=accumulate)
     torch.cuda.synchronize()
     assert sta.sta_get_device_error() == sta.STA_ERR_BAD_CACHE
-    want = K.attend(c, q.double().cpu().numpy(), 64 ** -0.5, [[[0, 2, 3]], [[0, 1, 2]], [[]], [[]]], True)
+    want = K.attend(c, q.double().cpu().numpy(), 64 ** -0.5, [[[0, 2, 3]], [[0, 1, 2]], [[]], [[]]], accumulate)
     rel = C.check_attention(o, lse, want, 64, "bf16", 200)
     C.check_weight(t, c, before, rel, 1)
 
@@ -260,13 +273,14 @@ def test_non_finite_values_of_a_newer_token(sta):
 
 @pytest.mark.parametrize("d,group,n_q,kv", [(64, 1, 4, 2), (128, 5, 3, 1), (128, 4, 6, 1), (64, 8, 8, 1),
                                             (128, 1, 64, 1)])
+@pytest.mark.parametrize("max_pages", [None, 700])
 @pytest.mark.parametrize("what", ["k_pages", "v_pages"])
-def test_non_finite_draft_tokens(sta, d, group, n_q, kv, what):
+def test_non_finite_draft_tokens(sta, d, group, n_q, kv, what, max_pages):
     """Every second one of the newest tokens has a key or a value that is not
     finite: a query is touched by those it sees and by no others, whatever
     page and piece of a page they lie in."""
     lens = [n_q, 33, 64, 65, 70, 96, 127, 200]
-    t = C.make(lens, kv, d, "bf16", seed=50 + n_q)
+    t = C.make(lens, kv, d, "bf16", seed=50 + n_q, max_pages=max_pages)
     q = C.queries(len(lens), n_q, kv * group, d, "bf16", seed=51)
     for b, n in enumerate(lens):
         for i in range(1, n_q, 2):

@@ -54,11 +54,11 @@ struct Args {
 
 // ------------------------------------------------------------------- append
 constexpr int APPEND_THREADS = 256;
-constexpr int APPEND_UNROLL = 4;
 
-// grid.y = sequence; each thread moves APPEND_UNROLL 16-byte chunks of the
-// sequence's new K and of its new V: reads run through the raster rows in
-// order, writes are the 2*D-byte rows of the heads' pages.
+// grid.y = sequence; each thread moves one 16-byte chunk of the sequence's new K
+// and one of its new V: reads run through the raster rows in order, writes are
+// the 2*D-byte rows of the heads' pages. (Two or four chunks to a thread: 219
+// and 222 us where one takes 216, 1.35 GB.)
 template <int D>
 __global__ void __launch_bounds__(APPEND_THREADS)
 append_kernel(Args a, const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new, int n_new,
@@ -72,40 +72,29 @@ append_kernel(Args a, const uint4 *__restrict__ k_new, const uint4 *__restrict__
     if (threadIdx.x == 0) record_error(DEV_ERR_BAD_CACHE);
     return;
   }
-  const unsigned total = (unsigned)c * a.H * CPR;
-  const unsigned base = blockIdx.x * (APPEND_THREADS * APPEND_UNROLL) + threadIdx.x;
-  const long long src0 = (long long)b * n_new * a.H * CPR;
-  uint4 k[APPEND_UNROLL], v[APPEND_UNROLL];
-  long long dst[APPEND_UNROLL];
-#pragma unroll
-  for (int u = 0; u < APPEND_UNROLL; ++u) {
-    const unsigned idx = base + u * APPEND_THREADS;
-    dst[u] = -1;
-    if (idx < total) {
-      k[u] = __ldcs(k_new + src0 + idx);
-      v[u] = __ldcs(v_new + src0 + idx);
-      const unsigned chunk = idx % CPR, th = idx / CPR;
-      const unsigned i = th / (unsigned)a.H, h = th - i * a.H;
-      const int r = b * a.H + (int)h;
-      const int len = a.length(r);
-      if (len >= 0 && len < c) record_error(DEV_ERR_BAD_CACHE);
-      if (len >= c) {
-        const int j = len - c + (int)i;
-        const int p = a.page(b, j);
-        if (p >= 0) dst[u] = a.row(p, (int)h, j) * CPR + chunk;
-        if (chunk == 0) {
-          if (a.pos != nullptr) a.pos[a.slot(r, j)] = a.seen[r] - c + (int)i;
-          if (a.weight != nullptr) a.weight[a.slot(r, j)] = 0.0f;
-        }
-      }
-    }
+  const unsigned idx = blockIdx.x * APPEND_THREADS + threadIdx.x;
+  if (idx >= (unsigned)c * a.H * CPR) return;
+  const long long src = (long long)b * n_new * a.H * CPR + idx;
+  const uint4 k = __ldcs(k_new + src), v = __ldcs(v_new + src);
+  const unsigned chunk = idx % CPR, th = idx / CPR;
+  const int i = (int)(th / (unsigned)a.H), h = (int)th - i * a.H;
+  const int r = b * a.H + h;
+  const int len = a.length(r);
+  if (len < c) {  // (-1: recorded)
+    if (len >= 0) record_error(DEV_ERR_BAD_CACHE);
+    return;
   }
-#pragma unroll
-  for (int u = 0; u < APPEND_UNROLL; ++u)
-    if (dst[u] >= 0) {
-      a.k[dst[u]] = k[u];
-      a.v[dst[u]] = v[u];
-    }
+  const int j = len - c + i;
+  const int p = a.page(b, j);
+  if (p >= 0) {
+    const long long dst = a.row(p, h, j) * CPR + chunk;
+    a.k[dst] = k;
+    a.v[dst] = v;
+  }
+  if (chunk == 0) {
+    if (a.pos != nullptr) a.pos[a.slot(r, j)] = a.seen[r] - c + i;
+    if (a.weight != nullptr) a.weight[a.slot(r, j)] = 0.0f;
+  }
 }
 
 // -------------------------------------------------------------------- evict
@@ -405,8 +394,8 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
   }
 }
 
-constexpr int MOVE_THREADS = 256;
-constexpr int MOVE_UNROLL = 4;
+constexpr int MOVE_THREADS = 128;
+constexpr int MOVE_UNROLL = 3;
 // Pairs one CTA of move_kernel<D> takes at a time.
 template <int D>
 __host__ __device__ constexpr int move_share() {

@@ -924,8 +924,7 @@ sta_status sta_cache_append(const sta_kv_cache *cache, const void *k_new, const 
   if (sm100_count() == 0) return STA_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const long long chunks = (long long)n_new * cache->kv_heads * (cache->d / 8);
-  const long long per_cta = cache::APPEND_THREADS * cache::APPEND_UNROLL;
-  const dim3 grid((unsigned)((chunks + per_cta - 1) / per_cta), (unsigned)cache->B);
+  const dim3 grid((unsigned)((chunks + cache::APPEND_THREADS - 1) / cache::APPEND_THREADS), (unsigned)cache->B);
   const uint4 *kn = static_cast<const uint4 *>(k_new), *vn = static_cast<const uint4 *>(v_new);
   return cache->d == 128
              ? launch_early(cache::append_kernel<128>, grid, cache::APPEND_THREADS, 0, 0, s, a, kn, vn, n_new, counts)
@@ -992,7 +991,6 @@ sta_status sta_cache_evict(const sta_kv_cache *cache, int32_t budget, int32_t re
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || ws_bytes < w.total)
     return STA_ERR_WORKSPACE;
   if (sm100_count() == 0) return STA_ERR_UNSUPPORTED;
-  if (w.cap == 0) return STA_OK;  // the page table holds no more than the budget
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   int *holes = reinterpret_cast<int *>(ws + w.holes), *fills = reinterpret_cast<int *>(ws + w.fills);
@@ -1007,7 +1005,7 @@ sta_status sta_cache_evict(const sta_kv_cache *cache, int32_t budget, int32_t re
                            : launch_plan<512, 64>(cache, a, budget, recent, sinks, w.cap, holes, fills, count, s);
   const sta_status run = small ? launch_plan<512, 0>(cache, a, budget, recent, sinks, w.cap, holes, fills, count, s)
                                : launch_plan<1024, 0>(cache, a, budget, recent, sinks, w.cap, holes, fills, count, s);
-  if (run != STA_OK) return run;
+  if (run != STA_OK || w.cap == 0) return run;  // (0: the page table holds no more than the budget)
   return cache->d == 128 ? launch_move<128>(cache, a, w.cap, holes, fills, count, s)
                          : launch_move<64>(cache, a, w.cap, holes, fills, count, s);
 }

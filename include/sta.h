@@ -440,7 +440,8 @@ sta_status sta_cache_append(const sta_kv_cache *cache, const void *k_new, const 
  * (a relative error of 2^-16 bf16, 2^-22 fp16).
  * q_heads is a multiple of kv_heads, n_q * q_heads / kv_heads <= 64.
  * workspace: device, >= sta_attn_fwd_cached_workspace() bytes (0 for sizes the
- * call rejects), 256-aligned; nothing in it has to start at zero, and calls
+ * call rejects; with accumulate 256 bytes for every page, head and query row),
+ * 256-aligned; nothing in it has to start at zero, and calls
  * that overlap on the GPU need one each. Deterministic. */
 size_t sta_attn_fwd_cached_workspace(const sta_kv_cache *cache, int32_t q_heads, int32_t n_q, int32_t accumulate);
 sta_status sta_attn_fwd_cached(const sta_kv_cache *cache, const void *q, void *o, float *lse, int32_t q_heads,

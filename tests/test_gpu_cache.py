@@ -337,6 +337,31 @@ def test_a_wait_that_runs_out_is_reported(sta):
         assert torch.equal(t["weight"], weight)
 
 
+def test_a_wait_that_runs_out_in_a_cluster(sta):
+    """The same for short rows, whose CTAs wait for one another as well: every
+    SM fetches its 14 pages at once from a cache that has been driven out of
+    L2 (58 MB: some 9 us, 16 times the limit)."""
+    B, kv, d, n = 16, 8, 128, 850
+    k, v = (torch.randn(B * 14, kv, C.PAGE, d, device="cuda").bfloat16() for _ in range(2))
+    table = torch.randperm(B * 14, device="cuda").int().reshape(B, 14)
+    t = {"k_pages": k, "v_pages": v, "page_table": table, "seen": None, "slot_pos": None, "weight": None,
+         "lens": torch.full((B, kv), n, dtype=torch.int32, device="cuda")}
+    q = C.queries(B, 1, kv * 4, d, "bf16", seed=63)
+    first = attend(sta, t, q)
+    ok(sta)
+    try:
+        sta.sta_set_wait_limit(1000)
+        torch.empty(512 << 20, dtype=torch.uint8, device="cuda").fill_(1)
+        attend(sta, t, q)
+        torch.cuda.synchronize()
+        assert sta.sta_get_device_error() == sta.STA_ERR_TIMEOUT
+    finally:
+        sta.sta_set_wait_limit(0)
+    again = attend(sta, t, q)
+    ok(sta)
+    assert torch.equal(C.bits(first[0]), C.bits(again[0])) and torch.equal(first[1], again[1])
+
+
 def test_large_scores_and_a_given_scale(sta):
     """Scores of some hundreds: the maximum is taken off before the
     exponential; and one key far above the others."""
@@ -477,6 +502,8 @@ def shuffled(t, seed):
     (64, "bf16", [130], 1, 1, 0),
     (128, "bf16", [5000, 1024, 1025], 1024, 100, 16),
     (64, "bf16", [40, 50], 1000, 10, 10),
+    (64, "bf16", [5000, 50], 6000, 10, 10),
+    (128, "bf16", [5000, 5060, 4990], 5000, 10, 10),
 ])
 def test_evict(sta, d, dtype, lens, budget, recent, sinks):
     for order in (False, True):

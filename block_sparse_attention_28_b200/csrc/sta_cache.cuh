@@ -55,11 +55,11 @@ struct Args {
 // ------------------------------------------------------------------- append
 constexpr int APPEND_THREADS = 256;
 
-// grid.y = sequence; each thread moves one 16-byte chunk of the sequence's new K
-// and one of its new V: reads run through the raster rows in order, writes are
-// the 2*D-byte rows of the heads' pages. (Two or four chunks to a thread: 219
-// and 222 us where one takes 216, 1.35 GB.)
-template <int D>
+// grid.y = sequence; each thread moves a 16-byte chunk of the new K and one of
+// the new V (STRIDE: and goes on by the grid's width): reads run through the
+// raster rows in order, writes are the 2*D-byte rows of the heads' pages. (Two
+// or four chunks at once: 219 and 222 us where one takes 216, 1.35 GB.)
+template <int D, bool STRIDE>
 __global__ void __launch_bounds__(APPEND_THREADS)
 append_kernel(Args a, const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new, int n_new,
               const int *__restrict__ counts) {
@@ -72,28 +72,31 @@ append_kernel(Args a, const uint4 *__restrict__ k_new, const uint4 *__restrict__
     if (threadIdx.x == 0) record_error(DEV_ERR_BAD_CACHE);
     return;
   }
-  const unsigned idx = blockIdx.x * APPEND_THREADS + threadIdx.x;
-  if (idx >= (unsigned)c * a.H * CPR) return;
-  const long long src = (long long)b * n_new * a.H * CPR + idx;
-  const uint4 k = __ldcs(k_new + src), v = __ldcs(v_new + src);
-  const unsigned chunk = idx % CPR, th = idx / CPR;
-  const int i = (int)(th / (unsigned)a.H), h = (int)th - i * a.H;
-  const int r = b * a.H + h;
-  const int len = a.length(r);
-  if (len < c) {  // (-1: recorded)
-    if (len >= 0) record_error(DEV_ERR_BAD_CACHE);
-    return;
-  }
-  const int j = len - c + i;
-  const int p = a.page(b, j);
-  if (p >= 0) {
-    const long long dst = a.row(p, h, j) * CPR + chunk;
-    a.k[dst] = k;
-    a.v[dst] = v;
-  }
-  if (chunk == 0) {
-    if (a.pos != nullptr) a.pos[a.slot(r, j)] = a.seen[r] - c + i;
-    if (a.weight != nullptr) a.weight[a.slot(r, j)] = 0.0f;
+  const unsigned total = (unsigned)c * a.H * CPR;
+  for (unsigned idx = blockIdx.x * APPEND_THREADS + threadIdx.x; idx < total; idx += gridDim.x * APPEND_THREADS) {
+    const long long src = (long long)b * n_new * a.H * CPR + idx;
+    const uint4 k = __ldcs(k_new + src), v = __ldcs(v_new + src);
+    const unsigned chunk = idx % CPR, th = idx / CPR;
+    const int i = (int)(th / (unsigned)a.H), h = (int)th - i * a.H;
+    const int r = b * a.H + h;
+    const int len = a.length(r);
+    if (len < c) {  // (-1: recorded)
+      if (len >= 0) record_error(DEV_ERR_BAD_CACHE);
+      if (!STRIDE) break;
+      continue;
+    }
+    const int j = len - c + i;
+    const int p = a.page(b, j);
+    if (p >= 0) {
+      const long long dst = a.row(p, h, j) * CPR + chunk;
+      a.k[dst] = k;
+      a.v[dst] = v;
+    }
+    if (chunk == 0) {
+      if (a.pos != nullptr) a.pos[a.slot(r, j)] = a.seen[r] - c + i;
+      if (a.weight != nullptr) a.weight[a.slot(r, j)] = 0.0f;
+    }
+    if (!STRIDE) break;
   }
 }
 

@@ -623,6 +623,15 @@ EvictWs evict_ws_layout(const sta_kv_cache *c, int32_t budget) {
   return w;
 }
 
+// CTAs for each of n rows (or sequences) of which some may have nothing to do:
+// how much there is only the device knows, and a CTA that finds none costs a
+// nanosecond. 64 per SM in all (evictions of 168 rows of 1 to 14,911 slots: 52
+// us, with a CTA for every pair that may be there 65, with 16 per SM 63).
+long long few_ctas(long long n) {
+  const long long share = (64 * decode::MAX_CTAS + n - 1) / n;
+  return share < 65535 ? share : 65535;
+}
+
 // One CTA per row, or a cluster for long rows: of up to 8 CTAs as long as each
 // has 8192 slots and an SM to itself (40 rows of 75,600 slots: 3 CTAs each take
 // 149 us with the moves, 4, some of them two to an SM, 183), and as many as the
@@ -650,8 +659,8 @@ template <int D>
 sta_status launch_move(const sta_kv_cache *c, const cache::Args &a, int cap, const int *holes, const int *fills,
                        const int *count, cudaStream_t s) {
   const long long passes = ((long long)cap + cache::move_share<D>() - 1) / cache::move_share<D>();
-  return launch_early(cache::move_kernel<D>,
-                      dim3((unsigned)(c->B * c->kv_heads), (unsigned)(passes < 65535 ? passes : 65535)),
+  const long long rows = (long long)c->B * c->kv_heads, share = few_ctas(rows);
+  return launch_early(cache::move_kernel<D>, dim3((unsigned)rows, (unsigned)(passes < share ? passes : share)),
                       cache::MOVE_THREADS, 0, 0, s, a, cap, holes, fills, count);
 }
 
@@ -924,11 +933,23 @@ sta_status sta_cache_append(const sta_kv_cache *cache, const void *k_new, const 
   if (sm100_count() == 0) return STA_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const long long chunks = (long long)n_new * cache->kv_heads * (cache->d / 8);
-  const dim3 grid((unsigned)((chunks + cache::APPEND_THREADS - 1) / cache::APPEND_THREADS), (unsigned)cache->B);
+  const long long needed = (chunks + cache::APPEND_THREADS - 1) / cache::APPEND_THREADS, share = few_ctas(cache->B);
   const uint4 *kn = static_cast<const uint4 *>(k_new), *vn = static_cast<const uint4 *>(v_new);
-  return cache->d == 128
-             ? launch_early(cache::append_kernel<128>, grid, cache::APPEND_THREADS, 0, 0, s, a, kn, vn, n_new, counts)
-             : launch_early(cache::append_kernel<64>, grid, cache::APPEND_THREADS, 0, 0, s, a, kn, vn, n_new, counts);
+  // A padded batch may be mostly padding (64 sequences of 0 to 5,275 rows: 12.3
+  // us, with a CTA for every row that may be there 23.5); striding costs a
+  // prompt that fills the grid 5%.
+  if (counts != nullptr && cache->B > 1 && needed > share) {
+    const dim3 grid((unsigned)share, (unsigned)cache->B);
+    return cache->d == 128 ? launch_early(cache::append_kernel<128, true>, grid, cache::APPEND_THREADS, 0, 0, s, a, kn,
+                                          vn, n_new, counts)
+                           : launch_early(cache::append_kernel<64, true>, grid, cache::APPEND_THREADS, 0, 0, s, a, kn,
+                                          vn, n_new, counts);
+  }
+  const dim3 grid((unsigned)needed, (unsigned)cache->B);
+  return cache->d == 128 ? launch_early(cache::append_kernel<128, false>, grid, cache::APPEND_THREADS, 0, 0, s, a, kn,
+                                        vn, n_new, counts)
+                         : launch_early(cache::append_kernel<64, false>, grid, cache::APPEND_THREADS, 0, 0, s, a, kn,
+                                        vn, n_new, counts);
 }
 
 size_t sta_attn_fwd_cached_workspace(const sta_kv_cache *cache, int32_t q_heads, int32_t n_q, int32_t accumulate) {

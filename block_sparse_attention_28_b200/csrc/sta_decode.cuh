@@ -10,8 +10,8 @@
 // and 8 query rows across: S^T = K Q^T, O^T = V^T P^T. (A tcgen05 tile has 64
 // rows at least; a token of a group of 1 to 8 heads has 8 to offer.)
 //
-// attend_kernel: one CTA per SM, 7 or 8 warps. A worker is a warp (two or four
-// for more than 16 or 32 query rows, 16 each) with a ring of its own in shared
+// attend_kernel: one CTA per SM, 7 or 8 warps. A worker is a warp (for many
+// query rows two or four, see rows_per_warp) with a ring of its own in shared
 // memory, into which its first warp sends half pages (TMA, 128-byte swizzle)
 // ahead of their use. The pages to be read, rows one after another, are cut
 // into one equal chunk per worker whatever the lengths are: no worker waits for
@@ -49,20 +49,33 @@ constexpr int MAX_STAGES = 28;          // of all workers
 constexpr int JOIN_BATCH = 4;
 constexpr long long DRAIN_LIMIT = 200000000LL;
 
-// Warps of a worker (16 query rows each) and workers of a CTA. Seven workers
-// of one warp have two stages of 16 KB each at d = 128, which is what shared
+// Query rows that a warp has: 16, and 32 at d = 64, where their outputs fit in
+// its registers. The keys and values are then read from shared memory by half
+// as many warps (8 sequences of 8,192 tokens, 8 key heads: with 20 query rows
+// 50 us, with 48 76 us; with 16 rows a warp 56 and 99).
+__host__ __device__ constexpr int rows_per_warp(int d, int M) { return d == 64 && M > 16 ? 32 : 16; }
+// Warps of a worker, workers of a CTA, stages of a worker's ring (16 KB at d =
+// 128, 8 at d = 64). Seven workers of one warp have 32 KB each: what shared
 // memory holds.
-__host__ __device__ inline int tiles_of(int M) { return M <= 16 ? 1 : (M <= 32 ? 2 : 4); }
-__host__ __device__ inline int workers_of(int M) { return M <= 16 ? 7 : (M <= 32 ? 4 : 2); }
-__host__ __device__ inline int warps_of(int M) { return tiles_of(M) * workers_of(M); }
+__host__ __device__ inline int tiles_of(int d, int M) {
+  const int warps = (M + rows_per_warp(d, M) - 1) / rows_per_warp(d, M);
+  return warps <= 2 ? warps : 4;
+}
+__host__ __device__ inline int workers_of(int d, int M) {
+  const int tiles = tiles_of(d, M);
+  return tiles == 1 ? 7 : 8 / tiles;
+}
+__host__ __device__ inline int stages_of(int d, int M) {
+  const int tiles = tiles_of(d, M);
+  return (tiles == 1 ? 2 : 3 * tiles / 2) * (128 / d);
+}
+inline int warps_of(int d, int M) { return tiles_of(d, M) * workers_of(d, M); }
 
 template <int D>
 struct Cfg {
   static constexpr int TILE_BYTES = HALF_BYTES * (D / 64);  // keys or values of a stage
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
-  // stages of a worker: 2, 3, 6 at d = 128, twice as many at d = 64
-  static __host__ __device__ inline int stages(int M) { return (M <= 16 ? 2 : (M <= 32 ? 3 : 6)) * (128 / D); }
-  static int smem(int M) { return 1024 + workers_of(M) * stages(M) * STAGE_BYTES; }
+  static int smem(int M) { return 1024 + workers_of(D, M) * stages_of(D, M) * STAGE_BYTES; }
 };
 
 struct Shape {
@@ -348,8 +361,8 @@ struct Producer {
 };
 
 // --------------------------------------------------------------- consumers
-// 8 NT query rows of one warp. Thread (g, t) = (lane / 4, lane % 4) holds, of
-// query rows 8 n + 2 t + y (y = 0, 1): o[c][n][y + 2 x], their outputs
+// 8 NT query rows of one warp (NT: 1, 2 or 4). Thread (g, t) = (lane / 4,
+// lane % 4) holds, of query rows 8 n + 2 t + y (y = 0, 1): o[c][n][y + 2 x], their outputs
 // 16 c + g + 8 x; the running maximum (log2); its share of the sum.
 template <int D, int NT>
 struct Tile {
@@ -630,7 +643,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
   __shared__ uint32_t abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rows = a.B * a.H, M = s.group * s.n_q;
-  const int tiles = tiles_of(M), workers = workers_of(M), stages = C::stages(M);
+  const int tiles = tiles_of(D, M), workers = workers_of(D, M), stages = stages_of(D, M);
   const int threads = blockDim.x;
   const int wk = warp / tiles, mt = warp % tiles, g = lane >> 2, t = lane & 3;
   cache::let_next_start();
@@ -724,7 +737,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
   p.ended = false;
   p.ok = true;
   if (mt == 0) p.find(a, s, rows, work);
-  const int m0 = 16 * mt, tile_rows = min(8 * NT, M - m0);  // may be <= 0
+  const int m0 = (NT == 4 ? 32 : 16) * mt, tile_rows = min(8 * NT, M - m0);  // may be <= 0
   int back[NT][2];  // newer tokens than the query row's
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -751,8 +764,9 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
     // The warp that sent the piece knows it already, and has the queries of a
     // new row on their way while it waits for the keys.
     __syncwarp();
-    Piece d = p.piece[stage];
-    if (mt == 0 && (d.flags & FIRST)) load_queries<D, NT, T>(q, a, s, d.row, m0, qb);
+    Piece d = {};
+    if (mt == 0) d = p.piece[stage];
+    if (d.flags & FIRST) load_queries<D, NT, T>(q, a, s, d.row, m0, qb);
     ok = __all_sync(0xFFFFFFFFu, wait(&p.full[stage], parity, &abort, limit));
     if (!ok) break;
     if (mt != 0) {

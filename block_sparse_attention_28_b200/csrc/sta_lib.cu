@@ -497,7 +497,7 @@ struct DecodeWs {
 DecodeWs decode_ws_layout(const sta_kv_cache *c, int group, int n_q, bool accumulate) {
   const size_t M = (size_t)group * n_q, rows = (size_t)c->B * c->kv_heads;
   const size_t units = accumulate ? rows * (c->max_pages + cache::ROW_COST) : 0;
-  const size_t parts = 2 * (size_t)decode::MAX_CTAS * decode::workers_of((int)M);
+  const size_t parts = 2 * (size_t)decode::MAX_CTAS * decode::workers_of(c->d, (int)M);
   DecodeWs w;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -528,7 +528,7 @@ int row_cluster(const sta_kv_cache *c, int M) {
   const long long rows = (long long)c->B * c->kv_heads;
   if (M > 8 || rows > decode::MAX_CTAS) return 0;
   const int ranks = rows <= 15 ? 8 : (rows <= 33 ? 4 : (rows <= 74 ? 2 : 1));
-  const int workers = decode::workers_of(M), mine = ranks * workers, all = decode::MAX_CTAS * workers;
+  const int workers = decode::workers_of(c->d, M), mine = ranks * workers, all = decode::MAX_CTAS * workers;
   const long long in_cluster = (c->max_pages + mine - 1) / mine;
   const long long in_general = (rows * (c->max_pages + cache::ROW_COST) + all - 1) / all;
   return in_cluster <= in_general && in_cluster <= 2 ? ranks : 0;
@@ -562,7 +562,7 @@ sta_status launch_decode(const sta_kv_cache *c, const cache::Args &a, const deco
       auto short_rows = decode::attend_kernel<D, 1, T, false, true>;
       STA_CUDA_TRY(cudaFuncSetAttribute(short_rows, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(M)));
       work.row_units = nullptr;
-      return launch_early(short_rows, dim3((unsigned)(c->B * c->kv_heads * ranks)), 32 * decode::warps_of(M), C::smem(M),
+      return launch_early(short_rows, dim3((unsigned)(c->B * c->kv_heads * ranks)), 32 * decode::warps_of(D, M), C::smem(M),
                           ranks, s, tk, tv, a, shape, static_cast<const T *>(q), sink, work, wait_limit());
     }
   }
@@ -570,7 +570,7 @@ sta_status launch_decode(const sta_kv_cache *c, const cache::Args &a, const deco
   const long long most = (long long)c->B * c->kv_heads * c->max_pages;
   const int sms = sm100_count() < decode::MAX_CTAS ? sm100_count() : decode::MAX_CTAS;
   const unsigned ctas = (unsigned)(most < sms ? most : sms);
-  sta_status st = launch_early(attend, dim3(ctas), 32 * decode::warps_of(M), C::smem(M), 0, s, tk, tv, a, shape,
+  sta_status st = launch_early(attend, dim3(ctas), 32 * decode::warps_of(D, M), C::smem(M), 0, s, tk, tv, a, shape,
                                static_cast<const T *>(q), sink, work, wait_limit());
   if (st != STA_OK) return st;
   // the fewer the rows, the fewer of their outputs to a CTA and the more
@@ -596,10 +596,15 @@ sta_status launch_decode(const sta_kv_cache *c, const cache::Args &a, const deco
 template <int D, typename T>
 sta_status launch_decode_any(const sta_kv_cache *c, const cache::Args &a, const decode::Shape &shape, const void *q,
                              void *o, float *lse, bool accumulate, uint8_t *ws, cudaStream_t s) {
-  // up to 8 query rows fill one tile of the products, more take two
-  if (shape.group * shape.n_q <= 8)
+  // tiles of 8 query rows that a warp has
+  const int M = shape.group * shape.n_q;
+  if (M <= 8)
     return accumulate ? launch_decode<D, 1, T, true>(c, a, shape, q, o, lse, ws, s)
                       : launch_decode<D, 1, T, false>(c, a, shape, q, o, lse, ws, s);
+  if constexpr (decode::rows_per_warp(D, decode::MAX_ROWS) == 32)
+    if (M > 16)
+      return accumulate ? launch_decode<D, 4, T, true>(c, a, shape, q, o, lse, ws, s)
+                        : launch_decode<D, 4, T, false>(c, a, shape, q, o, lse, ws, s);
   return accumulate ? launch_decode<D, 2, T, true>(c, a, shape, q, o, lse, ws, s)
                     : launch_decode<D, 2, T, false>(c, a, shape, q, o, lse, ws, s);
 }

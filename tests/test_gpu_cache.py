@@ -146,6 +146,7 @@ LENGTHS = [0, 1, 2, 63, 64, 65, 127, 128, 129, 700]
     (64, "bf16", 2, 1, 1), (128, "bf16", 1, 4, 1), (128, "fp16", 2, 8, 1), (64, "fp16", 1, 5, 3),
     (128, "bf16", 3, 1, 7), (64, "bf16", 1, 16, 4), (128, "fp16", 1, 1, 64), (128, "bf16", 2, 3, 9),
     (128, "bf16", 1, 64, 1), (64, "fp16", 2, 17, 1), (64, "bf16", 8, 1, 1), (128, "fp16", 12, 2, 1), (64, "fp16", 5, 2, 1),
+    (64, "bf16", 2, 8, 4), (64, "fp16", 1, 11, 3), (64, "bf16", 1, 3, 16),
 ])
 def test_attention_of_every_length(sta, d, dtype, kv, group, n_q, max_pages):
     t = C.make(LENGTHS, kv, d, dtype, seed=d + group + n_q, max_pages=max_pages)
@@ -155,7 +156,7 @@ def test_attention_of_every_length(sta, d, dtype, kv, group, n_q, max_pages):
 
 @pytest.mark.parametrize("d,dtype,kv,group,n_q", [
     (64, "bf16", 2, 1, 1), (128, "bf16", 1, 4, 1), (128, "fp16", 2, 8, 1), (64, "fp16", 1, 5, 3),
-    (128, "bf16", 1, 1, 40),
+    (128, "bf16", 1, 1, 40), (64, "bf16", 2, 4, 5), (64, "fp16", 1, 8, 4), (64, "bf16", 1, 16, 3),
 ])
 def test_accumulated_weight(sta, d, dtype, kv, group, n_q):
     t = C.make(LENGTHS, kv, d, dtype, seed=d + group + n_q)
@@ -272,7 +273,7 @@ def test_non_finite_values_of_a_newer_token(sta):
 
 
 @pytest.mark.parametrize("d,group,n_q,kv", [(64, 1, 4, 2), (128, 5, 3, 1), (128, 4, 6, 1), (64, 8, 8, 1),
-                                            (128, 1, 64, 1)])
+                                            (128, 1, 64, 1), (64, 4, 6, 1)])
 @pytest.mark.parametrize("max_pages", [None, 700])
 @pytest.mark.parametrize("what", ["k_pages", "v_pages"])
 def test_non_finite_draft_tokens(sta, d, group, n_q, kv, what, max_pages):

@@ -105,6 +105,8 @@ constexpr int PLAN_BINS = 2048;
 constexpr int PLAN_PASSES = 3;              // 11 + 11 + 10 bits of the key
 constexpr int PLAN_MAX_KEYS = 44 * 1024;    // keys a CTA holds in shared memory
 constexpr int PLAN_UNROLL = 8;
+// CTAs of a cluster, at most (rows that 512 threads take need one).
+__host__ __device__ constexpr int plan_ranks(int threads) { return threads == 1024 ? 8 : 1; }
 
 // Order of a slot as an unsigned key: the protected ones above every weight,
 // NaN below every weight, -0 as +0, else the weight's own order.
@@ -128,7 +130,7 @@ __device__ __forceinline__ int warp_scan(int v) {
 
 // Slots of a range by what becomes of them: equal to the threshold and below /
 // from the budget on; given up below it; kept from it on.
-struct Tally {
+struct alignas(16) Tally {
   int tie_below, tie_above, hole, fill;
   // Of the range's ties the first `take` stay (slot order: those below the
   // budget come first): its holes and fills.
@@ -195,14 +197,18 @@ __device__ __forceinline__ void move_pairs(const Args &a, int r, const int *hole
 // ties, holes (slots given up below the budget) and fills (slots kept above
 // it) per warp, and a last one lists holes and fills, both in slot order.
 // holes, fills [rows, cap], count [rows]. The length is updated here; the rest
-// by move_kernel, or (D > 0, one CTA per row) here as well. The key reads (8 bytes per slot) are the floor; what bounds
-// it is latency: some ten steps that each wait for the one before.
+// by move_kernel, or (D > 0, one CTA per row) here as well. The key reads (8
+// bytes per slot) are the floor; what bounds it is latency: some ten steps that
+// each wait for the one before (and, at 25,000 keys to a CTA, the instructions
+// of the five passes over them).
 template <int THREADS, int D>
 __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1)
 evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_room, int *holes, int *fills,
                   int *count) {
   constexpr int W = THREADS / 32;
   constexpr int PER = PLAN_BINS / THREADS;  // bins of a thread
+  constexpr int MOST = plan_ranks(THREADS);
+  constexpr int KEYS = THREADS == 1024 ? 4 : 2;  // keys of a thread read from shared memory at once: what registers hold
   extern __shared__ unsigned plan_smem[];
   unsigned *hist = plan_smem;                            // [PLAN_PASSES][PLAN_BINS]
   unsigned *keys = plan_smem + PLAN_PASSES * PLAN_BINS;  // [key_room]
@@ -226,7 +232,21 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
   const int *pos = a.pos + a.slot(r, begin);
   const float *weight = a.weight + a.slot(r, begin);
   auto read_key = [&](int j) { return evict_key(weight[j], pos[j], sinks, from); };
-  auto key_of = [&](int j) { return j < key_room ? keys[j] : read_key(j); };
+  // KEYS keys of this thread, `step` apart, from first + own on; those past
+  // n are read as anything. (512 threads have room for all keys.)
+  auto read_keys = [&](unsigned (&k)[KEYS], int first, int own, int step) {
+    const bool held = first + KEYS * step <= key_room;
+#pragma unroll
+    for (int x = 0; x < KEYS; ++x) {
+      const int j = first + own + x * step;
+      if (MOST == 1)
+        k[x] = j < n ? keys[j] : 0u;
+      else if (held)
+        k[x] = keys[j];
+      else
+        k[x] = j >= n ? 0u : (j < key_room ? keys[j] : read_key(j));
+    }
+  };
 
   for (int i = tid; i < PLAN_PASSES * PLAN_BINS; i += THREADS) hist[i] = 0;
   __syncthreads();
@@ -244,7 +264,7 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
       const int j = j0 + x * THREADS;
       if (j < n) {
         const unsigned k = evict_key(w[x], p[x], sinks, from);
-        if (j < key_room) keys[j] = k;
+        if (MOST == 1 || j < key_room) keys[j] = k;
         atomicAdd(&hist[k >> 21], 1u);
       }
     }
@@ -257,9 +277,13 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
     unsigned *mine = hist + pass * PLAN_BINS;
     if (pass > 0) {
       const int next = shift - bits;
-      for (int j = tid; j < n; j += THREADS) {
-        const unsigned k = key_of(j);
-        if ((k >> shift) == threshold) atomicAdd(&mine[(k >> next) & ((1u << bits) - 1u)], 1u);
+      for (int j0 = 0; j0 < n; j0 += THREADS * KEYS) {
+        unsigned k[KEYS];
+        read_keys(k, j0, tid, THREADS);
+#pragma unroll
+        for (int x = 0; x < KEYS; ++x)
+          if (j0 + tid + x * THREADS < n && (k[x] >> shift) == threshold)
+            atomicAdd(&mine[(k[x] >> next) & ((1u << bits) - 1u)], 1u);
       }
       shift = next;
     }
@@ -272,11 +296,13 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
     int sum[PER], all = 0;
 #pragma unroll
     for (int x = 0; x < PER; ++x) sum[x] = 0;
-    for (int c = 0; c < ranks; ++c) {
-      const unsigned *theirs = ranks > 1 ? cluster.map_shared_rank(mine, c) : mine;
 #pragma unroll
-      for (int x = 0; x < PER; ++x) sum[x] += (int)theirs[PLAN_BINS - 1 - PER * tid - x];
-    }
+    for (int c = 0; c < MOST; ++c)  // all CTAs' reads on their way at once
+      if (c < ranks) {
+        const unsigned *theirs = ranks > 1 ? cluster.map_shared_rank(mine, c) : mine;
+#pragma unroll
+        for (int x = 0; x < PER; ++x) sum[x] += (int)theirs[PLAN_BINS - 1 - PER * tid - x];
+      }
 #pragma unroll
     for (int x = 0; x < PER; ++x) all += sum[x];
     const int upto = warp_scan(all);
@@ -302,20 +328,27 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
   const int each = ((n + W - 1) / W + 31) / 32 * 32;  // a warp's slots
   const int lo = min(n, warp * each), hi = min(n, lo + each);
   const int edge = budget - begin;  // first local slot past the budget
+  const int mid = max(lo, min(edge, hi));
+  auto count_keys = [&](int first, int end, int &equal, int &less) {
+    for (int j0 = first; j0 < end; j0 += 32 * KEYS) {
+      unsigned k[KEYS];
+      read_keys(k, j0, lane, 32);
+#pragma unroll
+      for (int x = 0; x < KEYS; ++x) {
+        const bool in = j0 + lane + 32 * x < end;
+        equal += in && k[x] == threshold;
+        less += in && k[x] < threshold;
+      }
+    }
+  };
   Tally mine = {0, 0, 0, 0};
-#pragma unroll 4
-  for (int j = lo + lane; j < hi; j += 32) {
-    const unsigned k = key_of(j);
-    const bool below = j < edge;
-    mine.tie_below += k == threshold && below;
-    mine.tie_above += k == threshold && !below;
-    mine.hole += k < threshold && below;
-    mine.fill += k > threshold && !below;
-  }
+  int given_up = 0;  // at and past the budget
+  count_keys(lo, mid, mine.tie_below, mine.hole);
+  count_keys(mid, hi, mine.tie_above, given_up);
   mine.tie_below = __reduce_add_sync(0xFFFFFFFFu, mine.tie_below);
   mine.tie_above = __reduce_add_sync(0xFFFFFFFFu, mine.tie_above);
   mine.hole = __reduce_add_sync(0xFFFFFFFFu, mine.hole);
-  mine.fill = __reduce_add_sync(0xFFFFFFFFu, mine.fill);
+  mine.fill = hi - mid - mine.tie_above - __reduce_add_sync(0xFFFFFFFFu, given_up);
   if (lane == 0) tally[warp] = mine;
   __syncthreads();
   if (warp == 0) {
@@ -339,7 +372,15 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
     fill += v.fills(take);
     tie += v.ties();
   };
-  for (int c = 0; c < rank; ++c) pass_over(*cluster.map_shared_rank(&whole, c));
+  if (MOST > 1) {
+    Tally v[MOST];
+#pragma unroll
+    for (int c = 0; c < MOST; ++c)
+      if (c < rank) v[c] = *cluster.map_shared_rank(&whole, c);
+#pragma unroll
+    for (int c = 0; c < MOST; ++c)
+      if (c < rank) pass_over(v[c]);
+  }
   {
     Tally v = {0, 0, 0, 0};  // of warp `lane`, if it comes before this one
     if (lane < warp) v = tally[lane];
@@ -352,33 +393,36 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
   const unsigned below_lane = (1u << lane) - 1u;
   const bool no_ties = tally[warp].ties() == 0;
   int *hole_list = holes + (long long)r * cap, *fill_list = fills + (long long)r * cap;
-#pragma unroll 2
-  for (int j0 = lo; j0 < hi; j0 += 32) {
-    const int j = j0 + lane;
-    const bool in = j < hi;
-    const unsigned k = in ? key_of(j) : 0u;
-    bool keep = in && k > threshold;
-    if (!no_ties) {
-      const bool equal = in && k == threshold;
-      const unsigned eq = __ballot_sync(0xFFFFFFFFu, equal);
-      keep |= equal && tie + __popc(eq & below_lane) < left;
-      tie += __popc(eq);
+  // lists the slots of a range that are kept or given up; how many are listed then
+  auto list = [&](int first, int end, bool kept, int *to, int listed) {
+    for (int j0 = first; j0 < end; j0 += 32 * KEYS) {
+      unsigned k[KEYS];
+      bool keep[KEYS];
+      read_keys(k, j0, lane, 32);
+#pragma unroll
+      for (int x = 0; x < KEYS; ++x) keep[x] = k[x] > threshold;
+      if (!no_ties)
+#pragma unroll
+        for (int x = 0; x < KEYS; ++x) {
+          const bool equal = j0 + lane + 32 * x < end && k[x] == threshold;
+          const unsigned eq = __ballot_sync(0xFFFFFFFFu, equal);
+          keep[x] |= equal && tie + __popc(eq & below_lane) < left;
+          tie += __popc(eq);
+        }
+#pragma unroll
+      for (int x = 0; x < KEYS; ++x) {
+        const int j = j0 + lane + 32 * x;
+        const bool is = j < end && keep[x] == kept;
+        const unsigned mask = __ballot_sync(0xFFFFFFFFu, is);
+        const int at = listed + __popc(mask & below_lane);
+        if (is && at < cap) to[at] = begin + j;
+        listed += __popc(mask);
+      }
     }
-    if (j0 < edge) {
-      const bool is = in && !keep && j < edge;
-      const unsigned mask = __ballot_sync(0xFFFFFFFFu, is);
-      const int at = hole + __popc(mask & below_lane);
-      if (is && at < cap) hole_list[at] = begin + j;
-      hole += __popc(mask);
-    }
-    if (j0 + 32 > edge) {
-      const bool is = keep && j >= edge;
-      const unsigned mask = __ballot_sync(0xFFFFFFFFu, is);
-      const int at = fill + __popc(mask & below_lane);
-      if (is && at < cap) fill_list[at] = begin + j;
-      fill += __popc(mask);
-    }
-  }
+    return listed;
+  };
+  hole = list(lo, mid, false, hole_list, hole);
+  fill = list(mid, hi, true, fill_list, fill);
   if (rank == ranks - 1 && warp == W - 1 && lane == 0) {
     // as many holes as fills: `budget` slots stay in all (and never more than
     // the lists hold)

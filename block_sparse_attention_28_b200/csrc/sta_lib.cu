@@ -649,7 +649,8 @@ sta_status launch_plan(const sta_kv_cache *c, const cache::Args &a, int budget, 
   const long long need = (slots + cache::PLAN_MAX_KEYS - 1) / cache::PLAN_MAX_KEYS;
   long long ranks = fit < want ? fit : want;
   ranks = ranks > need ? ranks : need;
-  ranks = ranks < 1 ? 1 : (ranks > 8 ? 8 : ranks);
+  constexpr int MOST = cache::plan_ranks(THREADS);
+  ranks = ranks < 1 ? 1 : (ranks > MOST ? MOST : ranks);
   if (rows * ranks >= (1LL << 31)) return STA_ERR_UNSUPPORTED;
   const long long share = (slots / ranks + 63) / 32 * 32;
   const int room = (int)(share < cache::PLAN_MAX_KEYS ? share : cache::PLAN_MAX_KEYS);

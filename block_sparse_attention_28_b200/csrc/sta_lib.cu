@@ -639,7 +639,7 @@ long long few_ctas(long long n) {
 
 // One CTA per row, or a cluster for long rows: of up to 8 CTAs as long as each
 // has 8192 slots and an SM to itself (40 rows of 75,600 slots: 3 CTAs each take
-// 149 us with the moves, 4, some of them two to an SM, 183), and as many as the
+// 141 us with the moves, 4, some of them two to an SM, 161), and as many as the
 // keys need to fit in shared memory.
 template <int THREADS, int D>
 sta_status launch_plan(const sta_kv_cache *c, const cache::Args &a, int budget, int recent, int sinks, int cap,

@@ -39,7 +39,7 @@ def _nvcc():
 def sources():
     d = os.path.join(HERE, "csrc")
     inc = os.path.join(os.path.dirname(HERE), "include")
-    return [os.path.join(d, f) for f in sorted(os.listdir(d)) if f.endswith((".cu", ".cuh"))] + [
+    return [os.path.join(d, f) for f in sorted(os.listdir(d)) if f.endswith((".cu", ".cuh", ".h"))] + [
         os.path.join(inc, f) for f in sorted(os.listdir(inc)) if f.endswith(".h")]
 
 

@@ -424,10 +424,11 @@ def sta_attn_fwd_cached_workspace(cache, q_heads, n_q=1, accumulate=False):
 
 def sta_attn_fwd_cached(cache, q, o, lse, workspace, page_ptr=None, page_idx=None, accumulate=False, sm_scale=0.0,
                         stream=None):
-    """Attention of the newest tokens q [B, n_q, q_heads, d] over the cache, or
-    over the listed pages of each key head (CSR page_ptr int32
-    [B*kv_heads + 1], page_idx int32); accumulate adds each slot's attention
-    to cache.weight. workspace: uint8, sta_attn_fwd_cached_workspace() bytes."""
+    """Causal attention of the newest tokens q [B, n_q, q_heads, d] over the
+    cache, or over the listed pages of each key head (CSR page_ptr int32
+    [B*kv_heads + 1], page_idx int32): of the newest tokens each sees those up
+    to its own position (cache.slot_pos; without it, its own slot). accumulate
+    adds each slot's attention to cache.weight. workspace: uint8, sta_attn_fwd_cached_workspace() bytes."""
     B, n_q, q_heads, d = shape = q.shape if q.dim() == 4 else (0, 0, 0, 0)
     if B != cache.B or d != cache.d:
         raise ValueError(f"q: [{cache.B}, n_q, q_heads, {cache.d}], not {list(q.shape)}")

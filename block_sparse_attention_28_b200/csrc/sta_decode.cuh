@@ -3,6 +3,11 @@
 //   row r = (b, h): one key head; its M = n_q * group query rows, row
 //   m = i * group + g being token i of query head h * group + g
 //   s_j = scale q_m . k_j,  o_m = sum_j e^(s_j - lse_m) v_j
+// over the slots j that token i sees: all but those of the n_q - 1 - i newest
+// tokens, which go by their positions where the cache keeps them. A producer
+// then reads the positions of a piece's slots (4 bytes each) one piece ahead
+// and marks the few pieces that hold a token newer than the oldest query; only
+// in those (and where a row ends) the warps mask scores.
 //
 // Every key and value is read once and used by the M <= 64 query rows of its
 // head: at most 64 flop per byte, so HBM bounds the call. The matrix products
@@ -83,7 +88,17 @@ struct Shape {
   const int *page_ptr, *page_idx;  // page lists (CSR), or NULL
   long long idx_capacity;
   float scale_log2;  // scale * log2 e
+  // Which of the n_q newest tokens a slot holds: with more than one of them, by
+  // its position where positions are kept (an eviction moves the newest tokens
+  // into slots of any number), else by its slot.
+  bool by_position;
 };
+// How much newer than the oldest query a token is, given its position (or slot)
+// and the end of these (tokens seen, or slots filled): query i sees the tokens
+// up to i. The newest query sees every filled slot.
+__device__ __forceinline__ int newness(const Shape &s, int at, int end) {
+  return min((int)((unsigned)at - (unsigned)end) + s.n_q, s.n_q - 1);
+}
 
 struct Work {
   float *part_o;      // [2 * chunks][M][D]
@@ -100,11 +115,16 @@ struct Work {
 __device__ __forceinline__ int pack_page(int col, int held) { return col | (min(held, PAGE) - 1) << 24; }
 
 // What a worker's warps are told of a stage.
-enum : int { FIRST = 1, LAST = 2, WHOLE = 4, BEGINS = 8, SKIP = 16, END = 32, UPPER = 64 };
+enum : int { FIRST = 1, LAST = 2, WHOLE = 4, BEGINS = 8, SKIP = 16, END = 32, UPPER = 64, NEWER = 128 };
+constexpr int COLUMN = 8;  // flags' bits from here on: the page's column (below 2^24)
 struct __align__(16) Piece {
   int row, unit;
   int held;   // filled slots from the piece's first on (may be above KEYS)
-  int flags;  // UPPER: the page's second half
+  int flags;  // UPPER: the page's second half; NEWER: a slot is newer, by position, than the oldest query
+  // the piece's first slot
+  __device__ __forceinline__ int slot() const {
+    return (int)((unsigned)flags >> COLUMN) * PAGE + (flags & UPPER ? KEYS : 0);
+  }
 };
 
 // ------------------------------------------------------------ element types
@@ -243,6 +263,7 @@ struct Producer {
   int w_row, w_unit, w_held, w_flags, w_y;
   unsigned left;  // lanes of the batch still to be sent
   int upper;      // 1: the first of them has its lower half sent
+  int newer;      // of the next piece's slot `lane`, by position
 
   // Looks up the next units of the chunk, 32 at most.
   __device__ __forceinline__ void batch(const Args &a, const Shape &s, int rows, const Work &work) {
@@ -287,6 +308,7 @@ struct Producer {
       if (page >= 0) {
         w_y = (page * a.H + h) * PAGE;
         w_held = len - col * PAGE;
+        w_flags = (int)((unsigned)col << COLUMN);
       } else {
         col = -1;
         w_flags = SKIP;
@@ -316,6 +338,16 @@ struct Producer {
     while (left == 0 && u < u1 && row < rows) batch(a, s, rows, work);
   }
 
+  // Reads the positions of the next piece's slots: one piece ahead, so that
+  // they are there when it is sent (4 bytes of a slot against 4 D).
+  __device__ __forceinline__ void look_ahead(const Args &a, const Shape &s) {
+    if (!s.by_position || left == 0) return;
+    const int lane = threadIdx.x & 31, x = __ffs(left) - 1;
+    const int of = __shfl_sync(0xFFFFFFFFu, w_row, x);
+    const Piece next = {of, 0, 0, __shfl_sync(0xFFFFFFFFu, w_flags, x) | (upper ? UPPER : 0)};
+    newer = next.flags & SKIP ? 0 : newness(s, a.pos[a.slot(of, next.slot() + lane)], a.seen[of]);
+  }
+
   // Sends the next piece; where a chunk has no page, just the end.
   __device__ __forceinline__ void send(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, const Shape &s,
                                        int rows, const Work &work, volatile uint32_t *abort, long long limit) {
@@ -323,10 +355,14 @@ struct Producer {
     const bool none = left == 0;
     const int x = none ? 0 : __ffs(left) - 1;
     int state = 0;
+    bool any_newer = false;
+    if (s.by_position)
+      any_newer = __any_sync(0xFFFFFFFFu, lane < __shfl_sync(0xFFFFFFFFu, w_held, x) - upper * KEYS && newer > 0);
     if (lane == x) {
       const bool last = none || (w_flags & SKIP) || upper || w_held <= KEYS;
       int flags = none ? (SKIP | END) : w_flags;
       if (upper) flags = (flags & ~FIRST) | UPPER;
+      if (any_newer && !(flags & SKIP)) flags |= NEWER;
       if (!last) flags &= ~(LAST | END);
       if (issued < stages || wait(&empty[stage], ((issued / stages) & 1) ^ 1, abort, limit)) {
         piece[stage] = Piece{w_row, w_unit, w_held - upper * KEYS, flags};
@@ -357,6 +393,7 @@ struct Producer {
     } else {
       upper = 1;
     }
+    look_ahead(a, s);
   }
 };
 
@@ -418,16 +455,24 @@ struct Lanes {
   }
 };
 
-// One stage: scores, softmax step, weighted values. lim[n][y]: how many of its
-// slots query row 8 n + 2 t + y sees; held: how many are filled (either may be
-// negative or above KEYS). EDGE: any of these is below KEYS. scores: where
-// query row 0's scores go (MASS), of which the warp has `rows` rows.
+// One stage: scores, softmax step, weighted values. token[n][y]: the token (of
+// the n_q newest) that query row 8 n + 2 t + y is; held: how many of its slots
+// are filled (may be above KEYS). EDGE: some slot is not filled, or newer than
+// the oldest query; newer: of slot `lane` how much newer (newness; n_q: not
+// filled). scores: where query row 0's scores go (MASS), of which the warp has
+// `rows` rows.
 template <int D, int NT, typename T, bool MASS, bool EDGE>
 __device__ __forceinline__ void attend_slots(uint32_t stage, const Lanes &lanes, const uint32_t (&qb)[NT][D / 16][2],
-                                             const Shape &s, const int (&lim)[NT][2], int held, Tile<D, NT> &acc,
-                                             float *scores, int rows) {
+                                             const Shape &s, const int (&token)[NT][2], int held, int newer,
+                                             Tile<D, NT> &acc, float *scores, int rows) {
   using N = Num<T>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  int slot_newer[KT][2];  // of slots 16 x + g + 8 y
+  if (EDGE)
+#pragma unroll
+    for (int x = 0; x < KT; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) slot_newer[x][y] = __shfl_sync(0xFFFFFFFFu, newer, 16 * x + g + 8 * y);
   float p[KT][NT][4];
 #pragma unroll
   for (int x = 0; x < KT; ++x)
@@ -451,7 +496,7 @@ __device__ __forceinline__ void attend_slots(uint32_t stage, const Lanes &lanes,
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         p[x][n][e] = __fmul_rn(p[x][n][e], s.scale_log2);  // the score that is kept, with or without MASS
-        if (EDGE && 16 * x + g + 8 * (e >> 1) >= lim[n][e & 1]) p[x][n][e] = -INFINITY;
+        if (EDGE && slot_newer[x][e >> 1] > token[n][e & 1]) p[x][n][e] = -INFINITY;
       }
   if (MASS) {
 #pragma unroll
@@ -514,8 +559,8 @@ __device__ __forceinline__ void attend_slots(uint32_t stage, const Lanes &lanes,
   };
   bool odd = false;
   if (EDGE && s.n_q > 1) {
-    for (int key = max(0, held - (s.n_q - 1)); key < min(KEYS, held); ++key)
-      for (int d = lane; d < D; d += 32) odd |= (value(key, d) & N::NONFINITE) == N::NONFINITE;
+    for (unsigned some = __ballot_sync(0xFFFFFFFFu, newer > 0 && newer < s.n_q); some != 0; some &= some - 1)
+      for (int d = lane; d < D; d += 32) odd |= (value(__ffs(some) - 1, d) & N::NONFINITE) == N::NONFINITE;
     odd = __any_sync(0xFFFFFFFFu, odd);
   }
 #pragma unroll
@@ -560,7 +605,8 @@ __device__ __forceinline__ void attend_slots(uint32_t stage, const Lanes &lanes,
     }
   }
   if (EDGE && odd)
-    for (int key = 0; key < min(KEYS, held); ++key)
+    for (int key = 0; key < min(KEYS, held); ++key) {
+      const int key_newer = __shfl_sync(0xFFFFFFFFu, newer, key);
 #pragma unroll
       for (int c = 0; c < D / 16; ++c)
 #pragma unroll
@@ -571,8 +617,9 @@ __device__ __forceinline__ void attend_slots(uint32_t stage, const Lanes &lanes,
             for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int y = 0; y < 2; ++y)
-                if (key < lim[n][y]) acc.o[c][n][y + 2 * x] += N::unpack(v).x;
+                if (key_newer <= token[n][y]) acc.o[c][n][y + 2 * x] += N::unpack(v).x;
         }
+    }
 }
 
 // Where row m of row r's result goes.
@@ -736,15 +783,19 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
   p.left = 0;
   p.ended = false;
   p.ok = true;
-  if (mt == 0) p.find(a, s, rows, work);
+  p.newer = 0;
+  if (mt == 0) {
+    p.find(a, s, rows, work);
+    p.look_ahead(a, s);
+  }
   const int m0 = (NT == 4 ? 32 : 16) * mt, tile_rows = min(8 * NT, M - m0);  // may be <= 0
-  int back[NT][2];  // newer tokens than the query row's
+  int token[NT][2];  // of the n_q newest, a query row's
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
       const int m = m0 + 8 * n + 2 * t + y;
-      back[n][y] = m < M ? s.n_q - 1 - m / s.group : 0;
+      token[n][y] = m < M ? m / s.group : s.n_q - 1;
     }
   bool ok = true;
   Tile<D, NT> acc;
@@ -775,19 +826,22 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
     }
     if (d.flags & FIRST) acc.clear();
     if (!(d.flags & SKIP) && tile_rows > 0) {
-      int lim[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) lim[n][y] = d.held - back[n][y];
       const uint32_t at = ring + stage * C::STAGE_BYTES;
       float *sc = nullptr;
       if (MASS) dbg_ok(d.unit >= 0 && d.unit < units && d.row >= 0 && d.row < rows);
       if (MASS) sc = work.scores + ((long long)d.unit * M + m0) * PAGE + (d.flags & UPPER ? KEYS : 0);
-      if (d.held - (s.n_q - 1) < KEYS)
-        attend_slots<D, NT, T, MASS, true>(at, lanes, qb, s, lim, d.held, acc, sc, tile_rows);
-      else
-        attend_slots<D, NT, T, MASS, false>(at, lanes, qb, s, lim, d.held, acc, sc, tile_rows);
+      if (s.by_position ? d.held < KEYS || (d.flags & NEWER) : d.held - (s.n_q - 1) < KEYS) {
+        int newer = s.n_q;  // of slot `lane`
+        if (lane < d.held) {
+          if (!s.by_position)
+            newer = newness(s, lane, d.held);
+          else
+            newer = d.flags & NEWER ? newness(s, a.pos[a.slot(d.row, d.slot() + lane)], a.seen[d.row]) : 0;
+        }
+        attend_slots<D, NT, T, MASS, true>(at, lanes, qb, s, token, d.held, newer, acc, sc, tile_rows);
+      } else {
+        attend_slots<D, NT, T, MASS, false>(at, lanes, qb, s, token, d.held, 0, acc, sc, tile_rows);
+      }
     }
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&p.empty[stage]);

@@ -992,6 +992,7 @@ sta_status sta_attn_fwd_cached(const sta_kv_cache *cache, const void *q, void *o
   shape.page_ptr = page_ptr;
   shape.page_idx = page_idx;
   shape.idx_capacity = idx_capacity;
+  shape.by_position = n_q > 1 && a.pos != nullptr;
   shape.scale_log2 = (sm_scale != 0.0f ? sm_scale : 1.0f / sqrtf((float)cache->d)) * 1.4426950408889634f;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   const bool acc = accumulate != 0;

@@ -396,7 +396,8 @@ typedef struct {
                               ones included (= position of its next token), or
                               NULL when slot_pos is */
   int32_t *slot_pos;       /* [B, kv_heads, 64*max_pages] position of each slot's
-                              token, or NULL */
+                              token (attention of several tokens goes by it),
+                              or NULL */
   float *weight;           /* [B, kv_heads, 64*max_pages] attention weight each
                               slot's token has gathered, or NULL */
 } sta_kv_cache;
@@ -415,8 +416,8 @@ typedef struct {
 sta_status sta_cache_append(const sta_kv_cache *cache, const void *k_new, const void *v_new, int32_t n_new,
                             const int32_t *counts, sta_stream_t stream);
 
-/* sta_attn_fwd_cached -- attention of a sequence's newest tokens over its
- * cache (block-sparse when page lists are given).
+/* sta_attn_fwd_cached -- causal attention of a sequence's newest tokens over
+ * its cache (block-sparse when page lists are given).
  *   q, o    : [B, n_q, q_heads, d], not overlapping; the n_q newest tokens of
  *             each sequence, already appended; q head j reads key head
  *             j / (q_heads / kv_heads)
@@ -431,9 +432,15 @@ sta_status sta_cache_append(const sta_kv_cache *cache, const void *k_new, const 
  *   accumulate : 1: also add to weight[b][h][j] the attention that slot j got,
  *             sum over the queries i and the q heads of h of e^(s_j - lse);
  *             slots out of view get nothing added
- * With s_j = sm_scale q . k_j (sm_scale 0 means 1/sqrt(d)) over the slots j of
- * the listed pages that query i sees, j < lens - (n_q - 1 - i):
+ * With s_j = sm_scale q . k_j (sm_scale 0 means 1/sqrt(d)) over the filled
+ * slots j of the listed pages that query i sees:
  *   lse = log(sum_j e^(s_j)),  o = sum_j e^(s_j - lse) v_j.
+ * Query i does not see the n_q - 1 - i newest tokens. Where the cache keeps
+ * positions (slot_pos and seen given) those are the slots whose position is
+ * at least seen - (n_q - 1 - i), wherever they lie: sta_cache_evict moves the
+ * newest tokens too. Without positions they are the slots from
+ * lens - (n_q - 1 - i) on. The newest query (the only one, with n_q 1) sees
+ * every filled slot.
  * A query that sees no slot gives o = 0 and lse = -inf. What lies in slots out
  * of view (infinities and NaN included) has no effect. Sums are fp32; the
  * weights of the products with V are split in two terms of the cache's type
@@ -458,8 +465,9 @@ sta_status sta_attn_fwd_cached(const sta_kv_cache *cache, const void *q, void *o
  * from `budget` on takes the i-th slot given up below it, with its key, value,
  * position and weight. lens becomes `budget`; the slots behind are left as they
  * are, and the pages past ceil(budget / 64) are free once all heads are cut.
- * Slots are therefore not in order of position afterwards; attention does not
- * depend on it (the tokens appended since are the last ones).
+ * Slots are therefore not in order of position afterwards, the newest tokens
+ * among them; attention goes by position. Tokens appended since the last
+ * attention over them have no weight yet: recent >= their number keeps them.
  * Needs seen, slot_pos and weight. budget >= 1, recent >= 0, sinks >= 0,
  * recent + sinks <= budget. workspace: device, >= sta_cache_evict_workspace()
  * bytes, 256-aligned; nothing in it has to start at zero, and calls that

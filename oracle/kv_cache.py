@@ -31,11 +31,13 @@ def append(c, k_new, v_new, counts=None):
                     c["weight"][b, h, slot] = 0.0
 
 
-def attend(c, q, scale, lists=None, accumulate=False):
+def attend(c, q, scale, lists=None, accumulate=False, by_position=False):
     """(o, lse, sigma, terms): o [B, n_q, q_heads, d], lse [B, q_heads, n_q];
     for the tests' error bounds, sigma (like o) = sum_j p_j |v_j| and terms
     (like lse) = max_j of scale * sum_i |q_i k_ji|. lists[b][h]: the page
-    columns of a head, None: all."""
+    columns of a head, None: all. Query i of n_q does not see the n_q - 1 - i
+    newest tokens: the last slots or, by position, those at seen - (n_q - 1 - i)
+    and later (the newest query sees every slot)."""
     B, n_q, hq, d = q.shape
     kv = c["lens"].shape[1]
     group = hq // kv
@@ -46,7 +48,10 @@ def attend(c, q, scale, lists=None, accumulate=False):
             n = int(c["lens"][b, h])
             cols = range(-(-n // PAGE)) if lists is None else lists[b][h]
             for i in range(n_q):
-                slots = [j for p in cols for j in range(p * PAGE, min(n - (n_q - 1 - i), p * PAGE + PAGE))]
+                end = n if by_position else n - (n_q - 1 - i)
+                slots = [j for p in cols for j in range(p * PAGE, min(end, p * PAGE + PAGE))]
+                if by_position and i < n_q - 1:
+                    slots = [j for j in slots if c["slot_pos"][b, h, j] < c["seen"][b, h] - (n_q - 1 - i)]
                 if not slots:
                     continue
                 at = [where(c, b, j) for j in slots]

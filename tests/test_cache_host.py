@@ -266,3 +266,30 @@ def test_oracle_append_and_evict_by_hand():
     assert c["slot_pos"][0, 0, 4] == 6 and c["weight"][0, 0, 4] == 0
     assert (c["k_pages"][page, 0, 4] == 9).all() and (c["v_pages"][page, 0, 4] == -9).all()
     assert np.array_equal(c["k_pages"][page, 0, 5], k[5])
+
+
+def test_oracle_goes_by_position():
+    """Slots in order: as by slot. After an eviction, whose moves put new
+    tokens into earlier slots: dense causal attention over the kept tokens put
+    back in order of position."""
+    t = C.make([70, 130], 2, 64, "bf16", seed=3, device="cpu")
+    q = C.queries(2, 4, 4, 64, "bf16", seed=4, device="cpu").double().numpy()
+    c = C.oracle(t)
+    for x, y in zip(K.attend(c, q, 0.2), K.attend(c, q, 0.2, by_position=True)):
+        assert np.array_equal(x, y)
+    K.evict(c, 50, 4, 2)
+    pos = c["slot_pos"][:, :, :50]
+    assert (c["lens"] == 50).all() and any((pos[b, :, :46] >= n - 4).any() for b, n in ((0, 70), (1, 130)))
+    o, lse, _, _ = K.attend(c, q, 0.2, by_position=True)
+    for b in range(2):
+        for h in range(2):
+            order = np.argsort(pos[b, h])
+            at = [K.where(c, b, j) for j in order]
+            k = np.stack([c["k_pages"][p, h, r] for p, r in at])
+            v = np.stack([c["v_pages"][p, h, r] for p, r in at])
+            for g in (2 * h, 2 * h + 1):
+                s = 0.2 * q[b, :, g] @ k.T
+                s[np.arange(50)[None] > np.arange(46, 50)[:, None]] = -np.inf  # the last four are the newest
+                e = np.exp(s)
+                assert np.allclose(o[b, :, g], e / e.sum(1, keepdims=True) @ v, atol=1e-12)
+                assert np.allclose(lse[b, g], np.log(e.sum(1)), atol=1e-12)

@@ -24,7 +24,9 @@ STA_HD int filled_pages(int len) { return len > 0 ? (len - 1) / PAGE + 1 : 0; }
 STA_HD bool list_ok(int first, int next, long long capacity, int max_pages) {
   return first >= 0 && next >= first && next <= capacity && next - first <= max_pages;
 }
-// An entry of a list: a filled page, above the entry before it (-1: none).
+// An entry of a list: a filled page, above the largest entry before it (-1:
+// none). Comparing with all of them, not with the last one alone, is what keeps
+// a list out of order from naming a page twice.
 STA_HD bool column_ok(int column, int before, int filled) {
   return column >= 0 && column < filled && column > before;
 }

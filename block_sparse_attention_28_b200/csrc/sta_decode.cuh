@@ -263,7 +263,22 @@ struct Producer {
   int w_row, w_unit, w_held, w_flags, w_y;
   unsigned left;  // lanes of the batch still to be sent
   int upper;      // 1: the first of them has its lower half sent
+  int top;        // the largest entry before the next unit's in its row's list
   int newer;      // of the next piece's slot `lane`, by position
+
+  // The largest of a list's first n entries; -1: none.
+  __device__ __forceinline__ int largest(const Shape &s, int first, int n) const {
+    constexpr int UNROLL = 8;
+    int v = -1;
+    for (int j = threadIdx.x & 31; j < n; j += 32 * UNROLL) {
+      int e[UNROLL];
+#pragma unroll
+      for (int x = 0; x < UNROLL; ++x) e[x] = j + 32 * x < n ? s.page_idx[first + j + 32 * x] : -1;
+#pragma unroll
+      for (int x = 0; x < UNROLL; ++x) v = max(v, e[x]);
+    }
+    return __reduce_max_sync(0xFFFFFFFFu, v);
+  }
 
   // Looks up the next units of the chunk, 32 at most.
   __device__ __forceinline__ void batch(const Args &a, const Shape &s, int rows, const Work &work) {
@@ -290,19 +305,33 @@ struct Producer {
     const int len = __shfl_sync(0xFFFFFFFFu, mine.len, k), end = __shfl_sync(0xFFFFFFFFu, upto, k);
     const int i = n - (end - at);  // the row's i-th page; negative: the row's own unit
     const bool page_unit = lane < take && i >= 0;
+    int entry = i, before = -1;  // of the row's list, the largest before it
+    if (s.page_ptr != nullptr) {
+      if (page_unit) entry = s.page_idx[first + i];
+      if (u == u0) top = largest(s, __shfl_sync(0xFFFFFFFFu, first, 0), __shfl_sync(0xFFFFFFFFu, i, 0));
+      // the lanes before this one hold the entries before its own, up to the
+      // row's first or (i > lane) the batch's
+      int upto = page_unit ? entry : -1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o && i >= o) upto = max(upto, x);
+      }
+      if (i > lane) upto = max(upto, top);
+      const int x = __shfl_up_sync(0xFFFFFFFFu, upto, 1);
+      if (i > 0) before = lane > 0 ? x : top;
+      top = __shfl_sync(0xFFFFFFFFu, upto, take - 1);
+    }
     w_row = row + k;
     w_unit = u + lane;
     w_y = w_held = w_flags = 0;
     int col = -1;
     if (page_unit) {
       const int b = w_row / a.H, h = w_row - b * a.H, start = w_unit - i;
-      col = i;
-      if (s.page_ptr != nullptr) {
-        col = s.page_idx[first + i];
-        if (!cache::column_ok(col, i > 0 ? s.page_idx[first + i - 1] : -1, cache::filled_pages(len))) {
-          record_error(DEV_ERR_BAD_MASK);
-          col = -1;
-        }
+      col = entry;
+      if (s.page_ptr != nullptr && !cache::column_ok(entry, before, cache::filled_pages(len))) {
+        record_error(DEV_ERR_BAD_MASK);
+        col = -1;
       }
       const int page = col >= 0 ? a.page(b, col * PAGE) : -1;
       if (page >= 0) {
@@ -784,6 +813,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
   p.ended = false;
   p.ok = true;
   p.newer = 0;
+  p.top = -1;
   if (mt == 0) {
     p.find(a, s, rows, work);
     p.look_ahead(a, s);

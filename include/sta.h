@@ -425,10 +425,10 @@ sta_status sta_cache_append(const sta_kv_cache *cache, const void *k_new, const 
  *   page_ptr: optional device int32 [B*kv_heads + 1], page_idx int32
  *             [idx_capacity]: CSR over rows b*kv_heads + h of the page columns
  *             of page_table a head attends to, ascending and unique; NULL (both,
- *             idx_capacity 0): every page. An entry that is not above its
- *             predecessor, or past the last filled page, is skipped and
- *             recorded as STA_ERR_BAD_MASK, as are offsets that decrease or
- *             pass idx_capacity
+ *             idx_capacity 0): every page. An entry that is not above
+ *             every entry before it, or past the last filled page, is skipped
+ *             and recorded as STA_ERR_BAD_MASK, as are offsets that decrease
+ *             or pass idx_capacity
  *   accumulate : 1: also add to weight[b][h][j] the attention that slot j got,
  *             sum over the queries i and the q heads of h of e^(s_j - lse);
  *             slots out of view get nothing added

@@ -106,48 +106,42 @@ constexpr size_t MAX_DYN_SMEM = 227 * 1024;
 // of 64 d-values x 1 head x 8 columns x 8 rows x 1 frame is one token tile
 // (zero-filled beyond the grid edge), 128 B swizzle.
 bool make_raster_map(CUtensorMap *map, const void *base, const Geo &g, int B, int heads, int d) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
   const cuuint64_t row = (cuuint64_t)heads * d * 2;  // bytes per token
   cuuint64_t dims[5] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)g.W, (cuuint64_t)g.H,
                         (cuuint64_t)B * g.T};
   cuuint64_t strides[4] = {(cuuint64_t)d * 2, row, row * g.W, row * g.W * g.H};
   cuuint32_t box[5] = {64, 1, 8, 8, 1};
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5u, const_cast<void *>(base), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // Raster [B, L, heads, d] bf16 as the 5D tensor (d, heads, W, H, B*T) with a
 // box of a whole token tile for `hb` heads: d x hb x 8 x 8 x 1 (zero-filled
 // beyond the grid edge and the last head), no swizzle.
 bool make_raster_pool_map(CUtensorMap *map, const void *base, const Geo &g, int B, int heads, int d, int hb) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
   const cuuint64_t row = (cuuint64_t)heads * d * 2;  // bytes per token
   cuuint64_t dims[5] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)g.W, (cuuint64_t)g.H,
                         (cuuint64_t)B * g.T};
   cuuint64_t strides[4] = {(cuuint64_t)d * 2, row, row * g.W, row * g.W * g.H};
   cuuint32_t box[5] = {(cuuint32_t)d, (cuuint32_t)hb, 8, 8, 1};
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5u, const_cast<void *>(base), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // Pooled rows [bh, Nt, d] fp32 as a 3D tensor (d, Nt, bh); a box is 32 d-values
 // (128 B) x `rows` tiles x 1 head, zero-filled past Nt, 128 B swizzle.
 bool make_pooled_map(CUtensorMap *map, const float *base, long long bh, int nt, int d, int rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)nt, (cuuint64_t)bh};
   cuuint64_t strides[2] = {(cuuint64_t)d * 4, (cuuint64_t)nt * d * 4};
   cuuint32_t box[3] = {32, (cuuint32_t)rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3u, const_cast<float *>(base), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // Tensor-core scores S = scale * qbar kbar^T of every head into rows

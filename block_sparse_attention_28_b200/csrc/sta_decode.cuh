@@ -81,6 +81,7 @@ struct Cfg {
   static constexpr int TILE_BYTES = HALF_BYTES * (D / 64);  // keys or values of a stage
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
   static int smem(int M) { return 1024 + workers_of(D, M) * stages_of(D, M) * STAGE_BYTES; }
+  static int most_smem() { return smem(1); }  // seven workers of one warp
 };
 
 struct Shape {

@@ -528,6 +528,16 @@ int row_cluster(const sta_kv_cache *c, int M) {
   return in_cluster <= in_general && in_cluster <= 2 ? ranks : 0;
 }
 
+// Lets a kernel of the cache calls have up to `most` bytes of dynamic shared
+// memory. `most` is the kernel's own, whatever a call needs of it: a limit that
+// followed the call could be lowered by another thread's between here and the
+// launch.
+template <typename Kernel>
+sta_status allow_smem(Kernel *kernel, int most) {
+  STA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+  return STA_OK;
+}
+
 template <int D, int NT, typename T, bool MASS>
 sta_status launch_decode(const sta_kv_cache *c, const cache::Args &a, const decode::Shape &shape, const void *q,
                          void *o, float *lse, uint8_t *ws, cudaStream_t s) {
@@ -554,17 +564,18 @@ sta_status launch_decode(const sta_kv_cache *c, const cache::Args &a, const deco
   if constexpr (!MASS && NT == 1) {
     if (const int ranks = row_cluster(c, M); ranks > 0) {
       auto short_rows = decode::attend_kernel<D, 1, T, false, true>;
-      STA_CUDA_TRY(cudaFuncSetAttribute(short_rows, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(M)));
+      if (const sta_status st = allow_smem(short_rows, C::most_smem()); st != STA_OK) return st;
       work.row_units = nullptr;
       return launch_early(short_rows, dim3((unsigned)(c->B * c->kv_heads * ranks)), 32 * decode::warps_of(D, M), C::smem(M),
                           ranks, s, tk, tv, a, shape, static_cast<const T *>(q), sink, work, wait_limit());
     }
   }
-  STA_CUDA_TRY(cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(M)));
+  sta_status st = allow_smem(attend, C::most_smem());
+  if (st != STA_OK) return st;
   const long long most = (long long)c->B * c->kv_heads * c->max_pages;
   const int sms = sm100_count() < decode::MAX_CTAS ? sm100_count() : decode::MAX_CTAS;
   const unsigned ctas = (unsigned)(most < sms ? most : sms);
-  sta_status st = launch_early(attend, dim3(ctas), 32 * decode::warps_of(D, M), C::smem(M), 0, s, tk, tv, a, shape,
+  st = launch_early(attend, dim3(ctas), 32 * decode::warps_of(D, M), C::smem(M), 0, s, tk, tv, a, shape,
                                static_cast<const T *>(q), sink, work, wait_limit());
   if (st != STA_OK) return st;
   // the fewer the rows, the fewer of their outputs to a CTA and the more
@@ -577,8 +588,8 @@ sta_status launch_decode(const sta_kv_cache *c, const cache::Args &a, const deco
   // (one row in 929 parts: 33 us without it, 22.6 with it).
   const long long shares = (elements + wide - 1) / wide, per_sm = (rows * shares + sms - 1) / sms;
   const size_t spread = per_sm < 16 ? (size_t)(decode::JOIN_SPREAD / per_sm) : 0;
-  STA_CUDA_TRY(cudaFuncSetAttribute(decode::join_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    decode::JOIN_SPREAD));
+  st = allow_smem(decode::join_kernel<D, T>, decode::JOIN_SPREAD);
+  if (st != STA_OK) return st;
   st = launch_early(decode::join_kernel<D, T>, dim3((unsigned)rows, (unsigned)shares), decode::JOIN_THREADS, spread, 0,
                     s, a, shape, sink, work, wide);
   if (st != STA_OK || !MASS) return st;
@@ -648,9 +659,11 @@ sta_status launch_plan(const sta_kv_cache *c, const cache::Args &a, int budget, 
   if (rows * ranks >= (1LL << 31)) return STA_ERR_UNSUPPORTED;
   const long long share = (slots / ranks + 63) / 32 * 32;
   const int room = (int)(share < cache::PLAN_MAX_KEYS ? share : cache::PLAN_MAX_KEYS);
-  const size_t smem = ((size_t)cache::PLAN_PASSES * cache::PLAN_BINS + room) * sizeof(unsigned);
-  STA_CUDA_TRY(cudaFuncSetAttribute(cache::evict_plan_kernel<THREADS, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)smem));
+  constexpr int HIST = cache::PLAN_PASSES * cache::PLAN_BINS;
+  const size_t smem = ((size_t)HIST + room) * sizeof(unsigned);
+  const sta_status st = allow_smem(cache::evict_plan_kernel<THREADS, D>,
+                                   (HIST + cache::PLAN_MAX_KEYS) * (int)sizeof(unsigned));
+  if (st != STA_OK) return st;
   return launch_early(cache::evict_plan_kernel<THREADS, D>, dim3((unsigned)(rows * ranks)), THREADS, smem, (int)ranks, s,
                       a, budget, recent, sinks, cap, room, holes, fills, count);
 }

@@ -1,4 +1,6 @@
-"""Calls from host threads of their own."""
+"""Cache calls from several host threads at once, each on a stream, a cache and
+workspaces of its own: sizes that need different amounts of shared memory do
+not get into one another's way."""
 import threading
 
 import pytest
@@ -53,3 +55,33 @@ def test_the_first_call_of_a_thread(sta):  # noqa: F811
     ok(sta)
     assert torch.equal(C.bits(o), C.bits(want[0])) and torch.equal(lse, want[1])
     assert torch.equal(C.bits(outs[0]), C.bits(outs[1]))
+
+
+def test_attention_with_other_numbers_of_query_rows(sta):  # noqa: F811
+    t = C.make([300, 70], 1, 128, "bf16", seed=1, tracked=False, max_pages=700)
+    cache, works, outs = cache_of(sta, t), [], []
+    for n_q in (16, 40, 9, 64):
+        q = C.queries(2, n_q, 1, 128, "bf16", seed=n_q)
+        o, lse = torch.empty_like(q), torch.empty(2, 1, n_q, device="cuda")
+        ws, s = garbage(sta.sta_attn_fwd_cached_workspace(cache, 1, n_q)), torch.cuda.Stream()
+        outs.append((o, lse, attend(sta, t, q)))
+        works.append(lambda q=q, o=o, lse=lse, ws=ws, s=s: sta.sta_attn_fwd_cached(cache, q, o, lse, ws, stream=s))
+    torch.cuda.synchronize()
+    assert together(works, 2000) == []
+    ok(sta)
+    for o, lse, (want_o, want_lse) in outs:
+        assert torch.equal(C.bits(o), C.bits(want_o)) and torch.equal(lse, want_lse)
+
+
+def test_evictions_under_tables_of_other_widths(sta):  # noqa: F811
+    works, ends = [], []
+    for width, n in ((70, 4300), (300, 200), (640, 40_000), (66, 100)):
+        t = C.make([n], 1, 64, "bf16", seed=width, max_pages=max(width, -(-n // 64)), poison=False)
+        cache, s = cache_of(sta, t), torch.cuda.Stream()
+        ws = garbage(sta.sta_cache_evict_workspace(cache, n // 2))
+        ends.append((t, n // 2))
+        works.append(lambda c=cache, b=n // 2, ws=ws, s=s: sta.sta_cache_evict(c, b, 5, 1, ws, stream=s))
+    torch.cuda.synchronize()
+    assert together(works, 2000) == []
+    ok(sta)
+    assert all((t["lens"] == n).all() for t, n in ends)

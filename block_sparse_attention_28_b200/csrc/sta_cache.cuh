@@ -6,6 +6,8 @@
 #pragma once
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "sta_cache_index.h"
 #include "sta_common.cuh"
 
@@ -105,8 +107,7 @@ constexpr int PLAN_BINS = 2048;
 constexpr int PLAN_PASSES = 3;              // 11 + 11 + 10 bits of the key
 constexpr int PLAN_MAX_KEYS = 44 * 1024;    // keys a CTA holds in shared memory
 constexpr int PLAN_UNROLL = 8;
-// CTAs of a cluster, at most (rows that 512 threads take need one).
-__host__ __device__ constexpr int plan_ranks(int threads) { return threads == 1024 ? 8 : 1; }
+constexpr int PLAN_RANKS = 8;  // CTAs of a cluster, at most
 
 // Order of a slot as an unsigned key: the protected ones above every weight,
 // NaN below every weight, -0 as +0, else the weight's own order.
@@ -190,26 +191,33 @@ __device__ __forceinline__ void move_pairs(const Args &a, int r, const int *hole
   }
 }
 
-// A cluster of CTAs per (sequence, head), each with an equal range of the slots
-// and their keys in shared memory (read once; past key_room they are read
-// again). The budget-th largest key is found by radix selection on histograms
-// that every CTA sums up over the cluster; one more pass over the keys counts
-// ties, holes (slots given up below the budget) and fills (slots kept above
-// it) per warp, and a last one lists holes and fills, both in slot order.
-// holes, fills [rows, cap], count [rows]. The length is updated here; the rest
-// by move_kernel, or (D > 0, one CTA per row) here as well. The key reads (8
-// bytes per slot) are the floor; what bounds it is latency: some ten steps that
-// each wait for the one before (and, at 25,000 keys to a CTA, the instructions
-// of the five passes over them).
-template <int THREADS, int D>
-__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1)
-evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_room, int *holes, int *fills,
-                  int *count) {
+// What an eviction is asked for, and where its lists go.
+struct Evict {
+  int budget, recent, sinks;
+  int cap;              // pairs a row can have
+  int *holes, *fills;   // [rows][cap]
+  int *count;           // [rows] pairs that are left to move_kernel
+};
+
+// Plans row r, which has len > budget slots: a CTA, or (CLUSTER) those of a
+// cluster, each with an equal range of the slots and their keys in shared
+// memory (read once; past key_room they are read again). The budget-th largest
+// key is found by radix selection on histograms that every CTA sums up over the
+// cluster; one more pass over the keys counts ties, holes (slots given up below
+// the budget) and fills (slots kept above it) per warp, and a last one lists
+// holes and fills, both in slot order. The length is updated here; how many
+// pairs the row has is returned to the first thread of the last CTA's last warp
+// (0 to the others). The key reads (8 bytes per slot) are the floor; what bounds
+// it is latency: some ten steps that each wait for the one before (and, at
+// 25,000 keys to a CTA, the instructions of the five passes over them).
+template <int THREADS, bool CLUSTER>
+__device__ __forceinline__ int plan_row(const Args &a, const Evict &ev, int r, int len, unsigned *plan_smem,
+                                        int key_room) {
   constexpr int W = THREADS / 32;
   constexpr int PER = PLAN_BINS / THREADS;  // bins of a thread
-  constexpr int MOST = plan_ranks(THREADS);
+  constexpr int MOST = CLUSTER ? PLAN_RANKS : 1;
+  constexpr bool ROOM = THREADS == 512;  // for all keys
   constexpr int KEYS = THREADS == 1024 ? 4 : 2;  // keys of a thread read from shared memory at once: what registers hold
-  extern __shared__ unsigned plan_smem[];
   unsigned *hist = plan_smem;                            // [PLAN_PASSES][PLAN_BINS]
   unsigned *keys = plan_smem + PLAN_PASSES * PLAN_BINS;  // [key_room]
   __shared__ int part[W];
@@ -218,15 +226,9 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
   __shared__ int s_left;
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
-  const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int r = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  let_next_start();
-  wait_for_previous();
-  const int len = a.length(r), from = a.seen[r] - recent;
-  if (len <= budget) {  // for the whole cluster alike
-    if (D == 0 && tid == 0 && rank == 0) count[r] = 0;
-    return;
-  }
+  const int ranks = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int budget = ev.budget, sinks = ev.sinks, cap = ev.cap, from = a.seen[r] - ev.recent;
   const int seg = ((len + ranks - 1) / ranks + 31) / 32 * 32;
   const int begin = min(len, rank * seg), n = min(len, begin + seg) - begin;
   const int *pos = a.pos + a.slot(r, begin);
@@ -239,7 +241,7 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
 #pragma unroll
     for (int x = 0; x < KEYS; ++x) {
       const int j = first + own + x * step;
-      if (MOST == 1)
+      if (ROOM)
         k[x] = j < n ? keys[j] : 0u;
       else if (held)
         k[x] = keys[j];
@@ -264,7 +266,7 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
       const int j = j0 + x * THREADS;
       if (j < n) {
         const unsigned k = evict_key(w[x], p[x], sinks, from);
-        if (MOST == 1 || j < key_room) keys[j] = k;
+        if (ROOM || j < key_room) keys[j] = k;
         atomicAdd(&hist[k >> 21], 1u);
       }
     }
@@ -287,7 +289,7 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
       }
       shift = next;
     }
-    if (ranks > 1)
+    if (CLUSTER)
       cluster.sync();
     else
       __syncthreads();
@@ -299,7 +301,7 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
 #pragma unroll
     for (int c = 0; c < MOST; ++c)  // all CTAs' reads on their way at once
       if (c < ranks) {
-        const unsigned *theirs = ranks > 1 ? cluster.map_shared_rank(mine, c) : mine;
+        const unsigned *theirs = CLUSTER ? cluster.map_shared_rank(mine, c) : mine;
 #pragma unroll
         for (int x = 0; x < PER; ++x) sum[x] += (int)theirs[PLAN_BINS - 1 - PER * tid - x];
       }
@@ -360,39 +362,32 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
     v.fill = __reduce_add_sync(0xFFFFFFFFu, v.fill);
     if (lane == 0) whole = v;
   }
-  if (ranks > 1)
+  if (CLUSTER)
     cluster.sync();
   else
     __syncthreads();
   // ties, holes and fills before this warp's range
   int tie = 0, hole = 0, fill = 0;
-  auto pass_over = [&](const Tally &v) {
-    const int take = max(0, min(left - tie, v.ties()));
-    hole += v.holes(take);
-    fill += v.fills(take);
-    tie += v.ties();
-  };
-  if (MOST > 1) {
-    Tally v[MOST];
-#pragma unroll
-    for (int c = 0; c < MOST; ++c)
-      if (c < rank) v[c] = *cluster.map_shared_rank(&whole, c);
-#pragma unroll
-    for (int c = 0; c < MOST; ++c)
-      if (c < rank) pass_over(v[c]);
-  }
-  {
-    Tally v = {0, 0, 0, 0};  // of warp `lane`, if it comes before this one
-    if (lane < warp) v = tally[lane];
+  auto pass_over = [&](const Tally &v) {  // a lane's each, in the order of the lanes
     const int upto = warp_scan(v.ties());
     const int take = max(0, min(left - tie - (upto - v.ties()), v.ties()));
     hole += __reduce_add_sync(0xFFFFFFFFu, v.holes(take));
     fill += __reduce_add_sync(0xFFFFFFFFu, v.fills(take));
     tie += __shfl_sync(0xFFFFFFFFu, upto, 31);
+  };
+  if (CLUSTER) {
+    Tally v = {0, 0, 0, 0};  // of CTA `lane`
+    if (lane < rank) v = *cluster.map_shared_rank(&whole, lane);
+    pass_over(v);
+  }
+  {
+    Tally v = {0, 0, 0, 0};  // of warp `lane`
+    if (lane < warp) v = tally[lane];
+    pass_over(v);
   }
   const unsigned below_lane = (1u << lane) - 1u;
   const bool no_ties = tally[warp].ties() == 0;
-  int *hole_list = holes + (long long)r * cap, *fill_list = fills + (long long)r * cap;
+  int *hole_list = ev.holes + (long long)r * cap, *fill_list = ev.fills + (long long)r * cap;
   // lists the slots of a range that are kept or given up; how many are listed then
   auto list = [&](int first, int end, bool kept, int *to, int listed) {
     for (int j0 = first; j0 < end; j0 += 32 * KEYS) {
@@ -423,22 +418,112 @@ evict_plan_kernel(Args a, int budget, int recent, int sinks, int cap, int key_ro
   };
   hole = list(lo, mid, false, hole_list, hole);
   fill = list(mid, hi, true, fill_list, fill);
+  int pairs = 0;
   if (rank == ranks - 1 && warp == W - 1 && lane == 0) {
     // as many holes as fills: `budget` slots stay in all (and never more than
     // the lists hold)
-    const int pairs = min(min(hole, fill), cap);
-    if (D > 0)
-      s_left = pairs;
-    else
-      count[r] = pairs;
+    pairs = min(min(hole, fill), cap);
     a.lens[r] = budget;
   }
-  if (ranks > 1) cluster.sync();  // the others have read this CTA's memory
-  if constexpr (D > 0) {
+  // the others have read this CTA's memory, and its lists are written
+  if (CLUSTER)
+    cluster.sync();
+  else
     __syncthreads();
-    constexpr int SHARE = THREADS / (D / 8) * 2;
-    move_pairs<D, THREADS, 2>(a, r, hole_list, fill_list, s_left, 0, SHARE);
+  return pairs;
+}
+
+// Which kernel plans a row goes by the slots it holds, not by the width of the
+// page table, which a caller makes for the longest context it admits: up to
+// PLAN_SHORT slots 512 threads, three rows to an SM; more than those, 1024
+// threads or a cluster.
+constexpr int PLAN_SHORT = 4096;
+
+// A CTA per row of at most PLAN_SHORT slots, which also moves its pairs where
+// there are PLAN_MOVES at most, as in a cache that is cut at every step.
+constexpr int PLAN_MOVES = PAGE;
+template <int D>
+__global__ void __launch_bounds__(512, 3)
+evict_short_kernel(const Args a, const Evict ev, int key_room) {
+  extern __shared__ unsigned plan_smem[];
+  __shared__ int s_pairs;
+  const int r = blockIdx.x, tid = threadIdx.x;
+  let_next_start();
+  wait_for_previous();
+  const int len = a.length(r);
+  if (len <= ev.budget || len > PLAN_SHORT) {
+    if (tid == 0) ev.count[r] = 0;
+    return;
   }
+  const int got = plan_row<512, false>(a, ev, r, len, plan_smem, key_room);
+  if (tid == 512 - 32) {
+    s_pairs = got;
+    ev.count[r] = got <= PLAN_MOVES ? 0 : got;
+  }
+  __syncthreads();
+  if (s_pairs <= PLAN_MOVES)
+    move_pairs<D, 512, 2>(a, r, ev.holes + (long long)r * ev.cap, ev.fills + (long long)r * ev.cap, s_pairs, 0,
+                          512 / (D / 8) * 2);
+}
+
+// Rows of more than `above` slots (the others are evict_short_kernel's; -1:
+// there is none, and count is written for all rows). Those of up to `alone`
+// slots have a CTA each, the others a cluster; both stride over the rows. The
+// first warp looks for them, 32 lengths at a time, and leaves what it finds in
+// shared memory (held in registers it made the plan spill: 134 us at 40 rows of
+// 75,600 slots became 144). All CTAs of a cluster find the same rows: a row is
+// one cluster's alone, and its length changes only at the end of its plan.
+__global__ void __launch_bounds__(1024, 1)
+evict_long_kernel(const Args a, const Evict ev, int above, int alone, int key_room) {
+  extern __shared__ unsigned plan_smem[];
+  __shared__ int s_row[32], s_len[32], s_found;
+  __shared__ long long s_next;
+  namespace cg = cooperative_groups;
+  let_next_start();
+  wait_for_previous();
+  auto plan_rows = [&](auto with_cluster) {
+    constexpr bool TOGETHER = decltype(with_cluster)::value;
+    if (threadIdx.x == 0) {
+      const int ranks = (int)cg::this_cluster().num_blocks(), clusters = (int)gridDim.x / ranks;
+      s_next = (int)blockIdx.x / ranks + (TOGETHER ? 0 : (int)cg::this_cluster().block_rank() * clusters);
+    }
+    while (true) {
+      __syncthreads();
+      if (threadIdx.x < 32) {
+        const int lane = threadIdx.x, rows = a.B * a.H;
+        const int step = TOGETHER ? (int)gridDim.x / (int)cg::this_cluster().num_blocks() : (int)gridDim.x;
+        long long r0 = s_next;
+        unsigned todo = 0;
+        for (; todo == 0 && r0 < rows; r0 += 32LL * step) {
+          const long long mine = r0 + (long long)lane * step;
+          const int len = mine < rows ? (TOGETHER ? a.lens[mine] : a.length((int)mine)) : -1;
+          const bool cut = length_ok(len, a.max_pages) && len > ev.budget && len > above;
+          if (!TOGETHER && above < 0 && !cut && mine < rows) ev.count[mine] = 0;
+          todo = __ballot_sync(0xFFFFFFFFu, cut && (len > alone) == TOGETHER);
+          if (todo >> lane & 1) {
+            const int at = __popc(todo & ((1u << lane) - 1u));
+            s_row[at] = (int)mine;
+            s_len[at] = len;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) {
+          s_found = __popc(todo);
+          s_next = r0;
+        }
+      }
+      __syncthreads();
+      if (s_found == 0) break;
+      for (int i = 0; i < s_found; ++i) {
+        const int got = plan_row<1024, TOGETHER>(a, ev, s_row[i], s_len[i], plan_smem, key_room);
+        if (threadIdx.x == 1024 - 32 &&
+            (!TOGETHER || cg::this_cluster().block_rank() + 1 == cg::this_cluster().num_blocks()))
+          ev.count[s_row[i]] = got;
+      }
+    }
+  };
+  plan_rows(std::false_type{});
+  if (cg::this_cluster().num_blocks() > 1) plan_rows(std::true_type{});
 }
 
 constexpr int MOVE_THREADS = 128;
@@ -452,7 +537,7 @@ __host__ __device__ constexpr int move_share() {
 // grid.x = row, grid.y strides over its pairs.
 template <int D>
 __global__ void __launch_bounds__(MOVE_THREADS)
-move_kernel(Args a, int cap, const int *holes, const int *fills, const int *count) {
+move_kernel(const Args a, int cap, const int *holes, const int *fills, const int *count) {
   let_next_start();
   wait_for_previous();
   const int r = blockIdx.x;

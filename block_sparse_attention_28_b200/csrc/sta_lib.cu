@@ -633,48 +633,66 @@ EvictWs evict_ws_layout(const sta_kv_cache *c, int32_t budget) {
   return w;
 }
 
-// CTAs for each of n rows (or sequences) of which some may have nothing to do:
-// how much there is only the device knows, and a CTA that finds none costs a
-// nanosecond. 64 per SM in all (evictions of 168 rows of 1 to 14,911 slots: 52
-// us, with a CTA for every pair that may be there 65, with 16 per SM 63).
-long long few_ctas(long long n) {
-  const long long share = (64 * decode::MAX_CTAS + n - 1) / n;
+// CTAs for each of n rows (or sequences) of which some may have nothing to do,
+// `per_sm` for every SM in all.
+long long few_ctas(long long n, int per_sm) {
+  const long long share = ((long long)per_sm * decode::MAX_CTAS + n - 1) / n;
   return share < 65535 ? share : 65535;
 }
 
-// One CTA per row, or a cluster for long rows: of up to 8 CTAs as long as each
-// has 8192 slots and an SM to itself (40 rows of 75,600 slots: 3 CTAs each take
-// 141 us with the moves, 4, some of them two to an SM, 161), and as many as the
-// keys need to fit in shared memory.
-template <int THREADS, int D>
-sta_status launch_plan(const sta_kv_cache *c, const cache::Args &a, int budget, int recent, int sinks, int cap,
-                       int *holes, int *fills, int *count, cudaStream_t s) {
-  const long long rows = (long long)c->B * c->kv_heads, slots = (long long)cache::PAGE * c->max_pages;
-  const long long fit = decode::MAX_CTAS / rows, want = slots / 8192;
-  const long long need = (slots + cache::PLAN_MAX_KEYS - 1) / cache::PLAN_MAX_KEYS;
-  long long ranks = fit < want ? fit : want;
-  ranks = ranks > need ? ranks : need;
-  constexpr int MOST = cache::plan_ranks(THREADS);
-  ranks = ranks < 1 ? 1 : (ranks > MOST ? MOST : ranks);
-  if (rows * ranks >= (1LL << 31)) return STA_ERR_UNSUPPORTED;
-  const long long share = (slots / ranks + 63) / 32 * 32;
-  const int room = (int)(share < cache::PLAN_MAX_KEYS ? share : cache::PLAN_MAX_KEYS);
-  constexpr int HIST = cache::PLAN_PASSES * cache::PLAN_BINS;
-  const size_t smem = ((size_t)HIST + room) * sizeof(unsigned);
-  const sta_status st = allow_smem(cache::evict_plan_kernel<THREADS, D>,
-                                   (HIST + cache::PLAN_MAX_KEYS) * (int)sizeof(unsigned));
-  if (st != STA_OK) return st;
-  return launch_early(cache::evict_plan_kernel<THREADS, D>, dim3((unsigned)(rows * ranks)), THREADS, smem, (int)ranks, s,
-                      a, budget, recent, sinks, cap, room, holes, fills, count);
-}
+int plan_smem(int room) { return (cache::PLAN_PASSES * cache::PLAN_BINS + room) * (int)sizeof(unsigned); }
 
 template <int D>
-sta_status launch_move(const sta_kv_cache *c, const cache::Args &a, int cap, const int *holes, const int *fills,
-                       const int *count, cudaStream_t s) {
-  const long long passes = ((long long)cap + cache::move_share<D>() - 1) / cache::move_share<D>();
-  const long long rows = (long long)c->B * c->kv_heads, share = few_ctas(rows);
+sta_status launch_short_plan(const sta_kv_cache *c, const cache::Args &a, const cache::Evict &ev, cudaStream_t s) {
+  const long long slots = (long long)cache::PAGE * c->max_pages;
+  const int room = (int)(slots < cache::PLAN_SHORT ? slots : cache::PLAN_SHORT);
+  auto kernel = cache::evict_short_kernel<D>;
+  const sta_status st = allow_smem(kernel, plan_smem(cache::PLAN_SHORT));
+  if (st != STA_OK) return st;
+  return launch_early(kernel, dim3((unsigned)(c->B * c->kv_heads)), 512, plan_smem(room), 0, s, a, ev, room);
+}
+
+// Clusters of that many CTAs, an SM each, that a B200 holds at once.
+long long clusters_at_once(int ranks) { return ranks <= 3 ? decode::MAX_CTAS / ranks : (ranks == 4 ? 33 : 15); }
+
+// A CTA for a long row, or a cluster of up to 4 as long as all rows run at once
+// and each CTA has 8192 slots (40 rows of 75,600 slots: 3 CTAs each take 136 us
+// with the moves, 4, some of them two to an SM, 161; 18 rows of 100,000: 4 CTAs
+// 85, 8 125; one: 31 and 35), and as many as the keys need to fit in shared
+// memory. The size of the clusters goes by what the page table can hold,
+// whether a row takes one by what it holds: 8 rows of 20,000 slots take 21 us
+// under a table that just holds them (2 CTAs each) and 23 under one of 131,072.
+sta_status launch_long_plan(const sta_kv_cache *c, const cache::Args &a, const cache::Evict &ev, int above,
+                            cudaStream_t s) {
+  const long long rows = (long long)c->B * c->kv_heads, slots = (long long)cache::PAGE * c->max_pages;
+  int fit = 4;
+  while (fit > 1 && rows > clusters_at_once(fit)) --fit;
+  const long long want = slots / 8192, need = (slots + cache::PLAN_MAX_KEYS - 1) / cache::PLAN_MAX_KEYS;
+  long long most = fit < want ? fit : want;
+  most = most > need ? most : need;
+  const int ranks = (int)(most < 1 ? 1 : (most > cache::PLAN_RANKS ? cache::PLAN_RANKS : most));
+  // keys of a cluster's CTA, or of a row that has one for itself
+  long long share = (slots / ranks + 63) / 32 * 32;
+  share = fit > 1 && share < 2 * 8192 ? 2 * 8192 : share;
+  const int room = (int)(share < cache::PLAN_MAX_KEYS ? share : cache::PLAN_MAX_KEYS);
+  const int alone = fit > 1 ? 2 * 8192 - 1 : room;
+  const long long clusters = rows < clusters_at_once(ranks) ? rows : clusters_at_once(ranks);
+  const sta_status st = allow_smem(cache::evict_long_kernel, plan_smem(cache::PLAN_MAX_KEYS));
+  if (st != STA_OK) return st;
+  return launch_early(cache::evict_long_kernel, dim3((unsigned)(clusters * ranks)), 1024, plan_smem(room), ranks, s, a,
+                      ev, above, ranks == 1 ? cache::PAGE * c->max_pages : alone, room);
+}
+
+// How many pairs a row has only the device knows, and a CTA that finds none
+// costs a nanosecond: 64 CTAs per SM where each SM has a row at most, else 32
+// (168 rows of 1 to 14,911 slots: 64 per SM 30 us, 32 28, 16 30; 512 rows that
+// have moved their pairs already: 26, 21, 18; 40 rows of 75,600: 136, 138, 143).
+template <int D>
+sta_status launch_move(const sta_kv_cache *c, const cache::Args &a, const cache::Evict &ev, cudaStream_t s) {
+  const long long passes = ((long long)ev.cap + cache::move_share<D>() - 1) / cache::move_share<D>();
+  const long long rows = (long long)c->B * c->kv_heads, share = few_ctas(rows, rows <= decode::MAX_CTAS ? 64 : 32);
   return launch_early(cache::move_kernel<D>, dim3((unsigned)rows, (unsigned)(passes < share ? passes : share)),
-                      cache::MOVE_THREADS, 0, 0, s, a, cap, holes, fills, count);
+                      cache::MOVE_THREADS, 0, 0, s, a, ev.cap, ev.holes, ev.fills, ev.count);
 }
 
 }  // namespace
@@ -946,7 +964,7 @@ sta_status sta_cache_append(const sta_kv_cache *cache, const void *k_new, const 
   if (sm100_count() == 0) return STA_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const long long chunks = (long long)n_new * cache->kv_heads * (cache->d / 8);
-  const long long needed = (chunks + cache::APPEND_THREADS - 1) / cache::APPEND_THREADS, share = few_ctas(cache->B);
+  const long long needed = (chunks + cache::APPEND_THREADS - 1) / cache::APPEND_THREADS, share = few_ctas(cache->B, 64);
   const uint4 *kn = static_cast<const uint4 *>(k_new), *vn = static_cast<const uint4 *>(v_new);
   // A padded batch may be mostly padding (64 sequences of 0 to 5,275 rows: 12.3
   // us, with a CTA for every row that may be there 23.5); striding costs a
@@ -1028,21 +1046,28 @@ sta_status sta_cache_evict(const sta_kv_cache *cache, int32_t budget, int32_t re
   if (sm100_count() == 0) return STA_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  int *holes = reinterpret_cast<int *>(ws + w.holes), *fills = reinterpret_cast<int *>(ws + w.fills);
-  int *count = reinterpret_cast<int *>(ws + w.count);
-  // Short rows have 512 threads each, which also move the tokens where there
-  // are a page's at most, as in a cache that is cut at every step (512 rows cut
-  // by 64 tokens: 25.2 us, with the second kernel 26.3; 8 rows by 192: 14.1,
-  // 13.0).
-  const bool small = cache::PAGE * cache->max_pages <= 4096;
-  if (small && w.cap <= cache::PAGE)
-    return cache->d == 128 ? launch_plan<512, 128>(cache, a, budget, recent, sinks, w.cap, holes, fills, count, s)
-                           : launch_plan<512, 64>(cache, a, budget, recent, sinks, w.cap, holes, fills, count, s);
-  const sta_status run = small ? launch_plan<512, 0>(cache, a, budget, recent, sinks, w.cap, holes, fills, count, s)
-                               : launch_plan<1024, 0>(cache, a, budget, recent, sinks, w.cap, holes, fills, count, s);
-  if (run != STA_OK || w.cap == 0) return run;  // (0: the page table holds no more than the budget)
-  return cache->d == 128 ? launch_move<128>(cache, a, w.cap, holes, fills, count, s)
-                         : launch_move<64>(cache, a, w.cap, holes, fills, count, s);
+  cache::Evict ev;
+  ev.budget = budget;
+  ev.recent = recent;
+  ev.sinks = sinks;
+  ev.cap = w.cap;
+  ev.holes = reinterpret_cast<int *>(ws + w.holes);
+  ev.fills = reinterpret_cast<int *>(ws + w.fills);
+  ev.count = reinterpret_cast<int *>(ws + w.count);
+  // Rows of up to PLAN_SHORT slots have a kernel of their own where there are
+  // more rows than SMs (512 rows cut from 1,088 slots to 1,024 under a table of
+  // 4,160: 21 us, with evict_long_kernel alone 41) or no others.
+  const bool wide = cache::PAGE * cache->max_pages > cache::PLAN_SHORT;
+  const bool some_short =
+      !wide || (budget < cache::PLAN_SHORT && (long long)cache->B * cache->kv_heads > decode::MAX_CTAS);
+  sta_status run = STA_OK;
+  if (some_short)
+    run = cache->d == 128 ? launch_short_plan<128>(cache, a, ev, s) : launch_short_plan<64>(cache, a, ev, s);
+  if (run == STA_OK && wide) run = launch_long_plan(cache, a, ev, some_short ? cache::PLAN_SHORT : -1, s);
+  // (no row has more pairs than the lists hold)
+  if (run != STA_OK || w.cap == 0 || (!wide && w.cap <= cache::PLAN_MOVES)) return run;
+  return cache->d == 128 ? launch_move<128>(cache, a, ev, s)
+                         : launch_move<64>(cache, a, ev, s);
 }
 
 sta_status sta_set_wait_limit(int64_t limit_cycles) {

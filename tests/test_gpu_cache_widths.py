@@ -1,0 +1,171 @@
+"""Evictions of the same tokens under page tables of any width: a caller makes
+the table for the longest context it admits, and rows of every length lie in
+it side by side."""
+import pytest
+import torch
+
+import _cache as C
+from test_gpu_cache import cache_of, evict, garbage, ok, sta  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def make(lens, kv, width, seed, ties=False, d=64):
+    """A cache of sequences of lens[b] slots (or one for each head), positions
+    in any order, contents arbitrary bits."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    B = len(lens)
+    per_head = torch.tensor([[n] * kv if isinstance(n, int) else list(n) for n in lens], dtype=torch.int32,
+                            device="cuda")
+    need = [max(1, -(-int(x) // C.PAGE)) for x in per_head.amax(1)]
+    num, width = sum(need), max(width, max(need))
+    t = {n: torch.randint(-30000, 30000, (num, kv, C.PAGE, d), generator=g, device="cuda",
+                          dtype=torch.int16).view(torch.bfloat16) for n in ("k_pages", "v_pages")}
+    order = torch.randperm(num, generator=g, device="cuda").int()
+    table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+    for b in range(B):
+        table[b, :need[b]] = order[sum(need[:b]):sum(need[:b + 1])]
+    w = torch.rand(B, kv, C.PAGE * max(need), generator=g, device="cuda")
+    pos = torch.rand(w.shape, generator=g, device="cuda").argsort(-1).int()
+    if ties:
+        w = (w * 3).floor()
+    rest = C.PAGE * (width - max(need))
+    t.update(page_table=table, lens=per_head.contiguous(), seen=per_head.clone(),
+             weight=torch.nn.functional.pad(w, (0, rest)), slot_pos=torch.nn.functional.pad(pos, (0, rest)))
+    return t
+
+
+def expected(t, budget, recent, sinks):
+    """What the eviction makes of the cache, row by row."""
+    want = {n: x.clone() for n, x in t.items()}
+    for b, heads in enumerate(t["lens"].tolist()):
+        for h, n in enumerate(heads):
+            if n <= budget:
+                continue
+            p, x = t["slot_pos"][b, h, :n], t["weight"][b, h, :n].double()
+            key = torch.where((p < sinks) | (p >= int(t["seen"][b, h]) - recent), 1e9, x)
+            stay = torch.zeros(n, dtype=torch.bool, device="cuda")
+            stay[torch.sort(key, descending=True, stable=True).indices[:budget]] = True
+            to, of = (~stay[:budget]).nonzero()[:, 0], budget + stay[budget:].nonzero()[:, 0]
+            at = lambda j: (t["page_table"][b, j // C.PAGE].long(), h, j % C.PAGE)  # noqa: E731
+            for name in ("k_pages", "v_pages"):
+                want[name].view(torch.int16)[at(to)] = t[name].view(torch.int16)[at(of)]
+            for name in ("slot_pos", "weight"):
+                want[name][b, h, to] = t[name][b, h, of]
+            want["lens"][b, h] = budget
+    return want
+
+
+def same(t, want):
+    for name in ("k_pages", "v_pages"):
+        assert torch.equal(t[name].view(torch.int16), want[name].view(torch.int16)), name
+    for name in ("slot_pos", "weight", "lens", "seen"):
+        assert torch.equal(t[name], want[name]), name
+
+
+# what a row can hold around the borders between the kernels and their variants
+LENGTHS = [0, 1, 500, 501, 564, 4096, 4097, 5000, 16_383, 16_384, 20_000, 33_000]
+
+
+@pytest.mark.parametrize("width", [0, 1100, 6400])
+@pytest.mark.parametrize("kv,budget,recent,sinks", [
+    (1, 500, 40, 3),      # few rows: one kernel plans all of them
+    (1, 4096, 700, 9),    # no row of up to 4,096 slots is cut
+    (15, 500, 40, 3),     # more rows than SMs: two kernels
+    (15, 4500, 40, 3),
+    (15, 16_383, 0, 0),
+])
+@pytest.mark.parametrize("ties", [False, True])
+def test_rows_of_every_length(sta, kv, budget, recent, sinks, width, ties):  # noqa: F811
+    t = make(LENGTHS, kv, width, seed=kv + budget, ties=ties)
+    want = expected(t, budget, recent, sinks)
+    evict(sta, t, budget, recent, sinks)
+    ok(sta)
+    same(t, want)
+    evict(sta, t, budget, recent, sinks)  # nothing is over the budget now
+    ok(sta)
+    same(t, want)
+
+
+@pytest.mark.parametrize("width", [0, 3000])
+def test_rows_longer_than_a_cta_holds(sta, width):  # noqa: F811
+    """80 rows, of which a table this wide gives two CTAs (or more) to those
+    whose keys do not fit into one's memory."""
+    t = make([60_000, 100] + [(45_000, 45_100)] + [3000] * 37, 2, width, seed=3)
+    want = expected(t, 2500, 100, 4)
+    evict(sta, t, 2500, 100, 4)
+    ok(sta)
+    same(t, want)
+
+
+def test_heads_of_different_lengths(sta):  # noqa: F811
+    t = make([(100, 5000, 20_000), (4097, 0, 900)], 3, 700, seed=4)
+    want = expected(t, 600, 30, 2)
+    evict(sta, t, 600, 30, 2)
+    ok(sta)
+    same(t, want)
+
+
+@pytest.mark.parametrize("width", [0, 90, 900])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_rows_with_many_moves(sta, width, d):  # noqa: F811
+    """600 rows of up to some 1,000 pairs each: more than the CTAs of a row
+    take at a time."""
+    t = make([2600] * 20 + [1300] * 20 + [200] * 20, 10, width, seed=5, d=d)
+    want = expected(t, 1300, 10, 2)
+    moved = max((want["slot_pos"][b, 0] != t["slot_pos"][b, 0]).sum().item() for b in range(20))
+    share = 128 // (d // 8) * 3
+    assert moved > share * -(-32 * 148 // 600) or d == 64  # a second trip of a row's CTAs
+    evict(sta, t, 1300, 10, 2)
+    ok(sta)
+    same(t, want)
+
+
+def test_a_bad_length_is_recorded_under_any_table(sta):  # noqa: F811
+    for kv, width in ((2, 0), (2, 300), (160, 0), (160, 300)):
+        for budget in (100, 5000):
+            t = make([300, 200], kv, width, seed=6)
+            t["lens"][1, 1] = C.PAGE * t["page_table"].shape[1] + 1
+            t["lens"][0, 1] = -3
+            same_lens = t["lens"].clone()
+            evict(sta, t, budget, 10, 2)
+            torch.cuda.synchronize()
+            assert sta.sta_get_device_error() == sta.STA_ERR_BAD_CACHE
+            assert t["lens"][1, 1] == same_lens[1, 1] and t["lens"][0, 1] == -3
+            rest = t["lens"].flatten().tolist()
+            assert rest[2:kv] == [min(300, budget)] * (kv - 2) and t["lens"][1, 0] == min(200, budget)
+
+
+def test_a_wide_table_costs_little(sta):  # noqa: F811
+    """512 rows cut by 64 slots: under a table 15 times as wide within twice
+    the time (with a plan chosen by the table's width it was 2.6 times)."""
+    times = []
+    for width in (17, 256):
+        t = make([1088] * 64, 8, width, seed=7)
+        cache, full = cache_of(sta, t), t["lens"].clone()
+        ws = garbage(sta.sta_cache_evict_workspace(cache, 1024))
+
+        def work(cut):
+            for _ in range(20):
+                t["lens"].copy_(full)
+                if cut:
+                    sta.sta_cache_evict(cache, 1024, 128, 4, ws)
+
+        took = []
+        for cut in (False, True):
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                work(cut)
+            runs = []
+            for _ in range(15):
+                a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+                a.record()
+                graph.replay()
+                b.record()
+                b.synchronize()
+                runs.append(a.elapsed_time(b))
+            took.append(sorted(runs)[7])
+        times.append(took[1] - took[0])
+    ok(sta)
+    assert times[1] < 2 * times[0], times

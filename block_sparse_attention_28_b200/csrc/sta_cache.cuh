@@ -37,7 +37,9 @@ struct Args {
   // page of slot j of sequence b, or -1 (recorded) if it is not in the pool;
   // 0 <= j < PAGE * max_pages
   __device__ __forceinline__ int page(int b, int j) const {
-    const int p = table[(long long)b * max_pages + j / PAGE];
+    return checked_page(table[(long long)b * max_pages + j / PAGE]);
+  }
+  __device__ __forceinline__ int checked_page(int p) const {
     if (page_ok(p, num_pages)) return p;
     record_error(DEV_ERR_BAD_CACHE);
     return -1;

@@ -5,9 +5,9 @@
 //   s_j = scale q_m . k_j,  o_m = sum_j e^(s_j - lse_m) v_j
 // over the slots j that token i sees: all but those of the n_q - 1 - i newest
 // tokens, which go by their positions where the cache keeps them. A producer
-// then reads the positions of a piece's slots (4 bytes each) one piece ahead
-// and marks the few pieces that hold a token newer than the oldest query; only
-// in those (and where a row ends) the warps mask scores.
+// then reads the positions (4 bytes a slot) of the pages it looks up, a lane a
+// page's, and marks the few pieces that hold a token newer than the oldest
+// query; only in those (and where a row ends) the warps mask scores.
 //
 // Every key and value is read once and used by the M <= 64 query rows of its
 // head: at most 64 flop per byte, so HBM bounds the call. The matrix products
@@ -97,8 +97,8 @@ struct Shape {
 // How much newer than the oldest query a token is, given its position (or slot)
 // and the end of these (tokens seen, or slots filled): query i sees the tokens
 // up to i. The newest query sees every filled slot.
-__device__ __forceinline__ int newness(const Shape &s, int at, int end) {
-  return min((int)((unsigned)at - (unsigned)end) + s.n_q, s.n_q - 1);
+__device__ __forceinline__ int newness(int n_q, int at, int end) {
+  return min((int)((unsigned)at - (unsigned)end) + n_q, n_q - 1);
 }
 
 struct Work {
@@ -247,6 +247,47 @@ __device__ __forceinline__ RowPages row_pages(const Args &a, const Shape &s, int
 }
 
 // --------------------------------------------------------------- producer
+// The next two are calls: few of the kernel's calls need them, and their code
+// in line makes it start later behind other kernels (5 us in a step of 384 rows
+// of 1,300 slots).
+
+// Which halves of a page with `held` slots hold a token newer than the oldest
+// query: NEWER the lower, UPPER the upper.
+__device__ __noinline__ int newer_halves(const int *pos, int end, int n_q, int held) {
+  int halves = 0;
+  auto look = [&](int j, int at) {
+    if (j < held && newness(n_q, at, end) > 0) halves |= j < KEYS ? NEWER : UPPER;
+  };
+  if ((reinterpret_cast<uintptr_t>(pos) & 15u) == 0) {
+#pragma unroll 8
+    for (int j = 0; j < PAGE; j += 4) {
+      const int4 at = *reinterpret_cast<const int4 *>(pos + j);
+      look(j, at.x);
+      look(j + 1, at.y);
+      look(j + 2, at.z);
+      look(j + 3, at.w);
+    }
+  } else {
+#pragma unroll 4
+    for (int j = 0; j < PAGE; ++j) look(j, pos[j]);
+  }
+  return halves;
+}
+
+// The largest of a list's first n entries, for the whole warp; -1: none.
+__device__ __noinline__ int largest_entry(const int *list, int n) {
+  constexpr int UNROLL = 8;
+  int v = -1;
+  for (int j = threadIdx.x & 31; j < n; j += 32 * UNROLL) {
+    int e[UNROLL];
+#pragma unroll
+    for (int x = 0; x < UNROLL; ++x) e[x] = j + 32 * x < n ? list[j + 32 * x] : -1;
+#pragma unroll
+    for (int x = 0; x < UNROLL; ++x) v = max(v, e[x]);
+  }
+  return __reduce_max_sync(0xFFFFFFFFu, v);
+}
+
 // The first warp of a worker sends its pieces: 32 units at a time a lane each
 // finds its unit's row, column and page; the lanes then send them in order.
 template <int D>
@@ -265,21 +306,6 @@ struct Producer {
   unsigned left;  // lanes of the batch still to be sent
   int upper;      // 1: the first of them has its lower half sent
   int top;        // the largest entry before the next unit's in its row's list
-  int newer;      // of the next piece's slot `lane`, by position
-
-  // The largest of a list's first n entries; -1: none.
-  __device__ __forceinline__ int largest(const Shape &s, int first, int n) const {
-    constexpr int UNROLL = 8;
-    int v = -1;
-    for (int j = threadIdx.x & 31; j < n; j += 32 * UNROLL) {
-      int e[UNROLL];
-#pragma unroll
-      for (int x = 0; x < UNROLL; ++x) e[x] = j + 32 * x < n ? s.page_idx[first + j + 32 * x] : -1;
-#pragma unroll
-      for (int x = 0; x < UNROLL; ++x) v = max(v, e[x]);
-    }
-    return __reduce_max_sync(0xFFFFFFFFu, v);
-  }
 
   // Looks up the next units of the chunk, 32 at most.
   __device__ __forceinline__ void batch(const Args &a, const Shape &s, int rows, const Work &work) {
@@ -309,7 +335,7 @@ struct Producer {
     int entry = i, before = -1;  // of the row's list, the largest before it
     if (s.page_ptr != nullptr) {
       if (page_unit) entry = s.page_idx[first + i];
-      if (u == u0) top = largest(s, __shfl_sync(0xFFFFFFFFu, first, 0), __shfl_sync(0xFFFFFFFFu, i, 0));
+      if (u == u0) top = largest_entry(s.page_idx + __shfl_sync(0xFFFFFFFFu, first, 0), __shfl_sync(0xFFFFFFFFu, i, 0));
       // the lanes before this one hold the entries before its own, up to the
       // row's first or (i > lane) the batch's
       int upto = page_unit ? entry : -1;
@@ -334,11 +360,17 @@ struct Producer {
         record_error(DEV_ERR_BAD_MASK);
         col = -1;
       }
-      const int page = col >= 0 ? a.page(b, col * PAGE) : -1;
+      int page = -1, newer = 0;
+      if (col >= 0) {
+        // (both on their way at once)
+        const int given = a.table[(long long)b * a.max_pages + col];
+        if (s.by_position) newer = newer_halves(a.pos + a.slot(w_row, col * PAGE), a.seen[w_row], s.n_q, len - col * PAGE);
+        page = a.checked_page(given);
+      }
       if (page >= 0) {
         w_y = (page * a.H + h) * PAGE;
         w_held = len - col * PAGE;
-        w_flags = (int)((unsigned)col << COLUMN);
+        w_flags = (int)((unsigned)col << COLUMN) | newer;
       } else {
         col = -1;
         w_flags = SKIP;
@@ -368,16 +400,6 @@ struct Producer {
     while (left == 0 && u < u1 && row < rows) batch(a, s, rows, work);
   }
 
-  // Reads the positions of the next piece's slots: one piece ahead, so that
-  // they are there when it is sent (4 bytes of a slot against 4 D).
-  __device__ __forceinline__ void look_ahead(const Args &a, const Shape &s) {
-    if (!s.by_position || left == 0) return;
-    const int lane = threadIdx.x & 31, x = __ffs(left) - 1;
-    const int of = __shfl_sync(0xFFFFFFFFu, w_row, x);
-    const Piece next = {of, 0, 0, __shfl_sync(0xFFFFFFFFu, w_flags, x) | (upper ? UPPER : 0)};
-    newer = next.flags & SKIP ? 0 : newness(s, a.pos[a.slot(of, next.slot() + lane)], a.seen[of]);
-  }
-
   // Sends the next piece; where a chunk has no page, just the end.
   __device__ __forceinline__ void send(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, const Shape &s,
                                        int rows, const Work &work, volatile uint32_t *abort, long long limit) {
@@ -385,14 +407,13 @@ struct Producer {
     const bool none = left == 0;
     const int x = none ? 0 : __ffs(left) - 1;
     int state = 0;
-    bool any_newer = false;
-    if (s.by_position)
-      any_newer = __any_sync(0xFFFFFFFFu, lane < __shfl_sync(0xFFFFFFFFu, w_held, x) - upper * KEYS && newer > 0);
     if (lane == x) {
       const bool last = none || (w_flags & SKIP) || upper || w_held <= KEYS;
       int flags = none ? (SKIP | END) : w_flags;
-      if (upper) flags = (flags & ~FIRST) | UPPER;
-      if (any_newer && !(flags & SKIP)) flags |= NEWER;
+      if (upper)  // (w_flags has UPPER where the upper half holds a newer token)
+        flags = (flags & ~(FIRST | NEWER)) | UPPER | (flags & UPPER ? NEWER : 0);
+      else
+        flags &= ~UPPER;
       if (!last) flags &= ~(LAST | END);
       if (issued < stages || wait(&empty[stage], ((issued / stages) & 1) ^ 1, abort, limit)) {
         piece[stage] = Piece{w_row, w_unit, w_held - upper * KEYS, flags};
@@ -423,7 +444,6 @@ struct Producer {
     } else {
       upper = 1;
     }
-    look_ahead(a, s);
   }
 };
 
@@ -813,12 +833,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
   p.left = 0;
   p.ended = false;
   p.ok = true;
-  p.newer = 0;
   p.top = -1;
-  if (mt == 0) {
-    p.find(a, s, rows, work);
-    p.look_ahead(a, s);
-  }
+  if (mt == 0) p.find(a, s, rows, work);
   const int m0 = (NT == 4 ? 32 : 16) * mt, tile_rows = min(8 * NT, M - m0);  // may be <= 0
   int token[NT][2];  // of the n_q newest, a query row's
 #pragma unroll
@@ -865,9 +881,9 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
         int newer = s.n_q;  // of slot `lane`
         if (lane < d.held) {
           if (!s.by_position)
-            newer = newness(s, lane, d.held);
+            newer = newness(s.n_q, lane, d.held);
           else
-            newer = d.flags & NEWER ? newness(s, a.pos[a.slot(d.row, d.slot() + lane)], a.seen[d.row]) : 0;
+            newer = d.flags & NEWER ? newness(s.n_q, a.pos[a.slot(d.row, d.slot() + lane)], a.seen[d.row]) : 0;
         }
         attend_slots<D, NT, T, MASS, true>(at, lanes, qb, s, token, d.held, newer, acc, sc, tile_rows);
       } else {

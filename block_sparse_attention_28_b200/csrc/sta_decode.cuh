@@ -150,8 +150,9 @@ struct Num<__nv_bfloat16> {
 };
 template <>
 struct Num<__half> {
-  // p is scaled to at most 2^14 (the sum with it), so that fp16, whose
-  // smallest step is 2^-24, keeps weights down to 2^-38 of the largest
+  // p is scaled to at most 2^14 (the sum with it): fp16's smallest step is
+  // 2^-24, so the second of a weight's two terms is off by up to 2^-25, which
+  // is 2^-39 of the largest weight (more than 2^-22 of those below 2^-17 of it)
   static constexpr float SHIFT = 14.0f;
   static constexpr uint32_t NONFINITE = 0x7C00u;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {

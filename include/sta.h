@@ -443,8 +443,10 @@ sta_status sta_cache_append(const sta_kv_cache *cache, const void *k_new, const 
  * every filled slot.
  * A query that sees no slot gives o = 0 and lse = -inf. What lies in slots out
  * of view (infinities and NaN included) has no effect. Sums are fp32; the
- * weights of the products with V are split in two terms of the cache's type
- * (a relative error of 2^-16 bf16, 2^-22 fp16).
+ * weights of the products with V are split in two terms of the cache's type:
+ * off by up to 2^-16 of themselves in bf16, and in fp16, whose smallest step
+ * bounds the second term, by up to 2^-22 of themselves or 2^-39 of the query's
+ * largest weight, whichever is more.
  * q_heads is a multiple of kv_heads, n_q * q_heads / kv_heads <= 64.
  * workspace: device, >= sta_attn_fwd_cached_workspace() bytes (0 for sizes the
  * call rejects; with accumulate 256 bytes for every page, head and query row),

@@ -442,7 +442,8 @@ sta_status sta_cache_append(const sta_kv_cache *cache, const void *k_new, const 
  * lens - (n_q - 1 - i) on. The newest query (the only one, with n_q 1) sees
  * every filled slot.
  * A query that sees no slot gives o = 0 and lse = -inf. What lies in slots out
- * of view (infinities and NaN included) has no effect. Sums are fp32; the
+ * of view (infinities and NaN included) has no effect; in view, a value that
+ * is not finite makes the outputs it enters infinite or NaN. Sums are fp32; the
  * weights of the products with V are split in two terms of the cache's type:
  * off by up to 2^-16 of themselves in bf16, and in fp16, whose smallest step
  * bounds the second term, by up to 2^-22 of themselves or 2^-39 of the query's

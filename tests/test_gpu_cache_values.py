@@ -1,4 +1,5 @@
-"""What the two-term weights of the products with V leave of small weights."""
+"""What the two-term weights of the products with V leave of small weights, and
+what values that are not finite do."""
 import numpy as np
 import pytest
 import torch
@@ -45,3 +46,31 @@ def test_small_weights_beside_a_token_of_value_zero(sta, d, dtype):  # noqa: F81
     limit += np.maximum((want + limit) * C.HALF[dtype], tiny)
     got = o[0, 0, 0, 1:n].double().cpu().numpy()
     assert (np.abs(got - want) <= limit).all(), (got - want) / limit
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("d,group,n_q", [(64, 1, 1), (128, 4, 1), (64, 8, 4), (128, 2, 3)])
+def test_a_value_in_view_that_is_not_finite(sta, d, group, n_q, bad):  # noqa: F811
+    """A token that is the newest at first and then ages: the column of its value
+    that is not finite is not finite for every query that sees it, at any age;
+    all other columns are untouched."""
+    for age in (0, 1, 3, 70, 200):
+        lens = [age + 5, age + 90]
+        t = C.make(lens, 1, d, "bf16", seed=age)
+        for b, n in enumerate(lens):
+            j = n - 1 - age
+            t["v_pages"][int(t["page_table"][b, j // C.PAGE]), 0, j % C.PAGE, 7] = bad
+        q = C.queries(2, n_q, group, d, "bf16", seed=3)
+        o, lse = attend(sta, t, q)
+        ok(sta)
+        c = C.oracle(t)
+        sees = [i for i in range(n_q) if n_q - 1 - i <= age]
+        with np.errstate(invalid="ignore"):
+            want = K.attend(c, q.double().cpu().numpy(), d ** -0.5)
+        assert torch.isfinite(lse).all() and not torch.isfinite(o[:, sees][..., 7].float()).any()
+        keep = np.arange(d) != 7
+        part = tuple(x[..., keep] if x.ndim == 4 else x for x in want)
+        C.check_attention(o[..., keep], lse, part, d, "bf16", max(lens))
+        early = [i for i in range(n_q) if i not in sees]
+        if early:
+            assert torch.isfinite(o[:, early].float()).all()

@@ -46,13 +46,17 @@ struct Args {
   }
   // row (key or value of one token and head) of the pools
   __device__ __forceinline__ long long row(int page, int h, int j) const {
-    dbg_ok(page >= 0 && page < num_pages && h >= 0 && h < H && j >= 0);
     return ((long long)page * H + h) * PAGE + j % PAGE;
   }
   // index of slot j of row r in slot_pos and weight
-  __device__ __forceinline__ long long slot(int r, int j) const {
-    dbg_ok(r >= 0 && r < B * H && j >= 0 && j < PAGE * max_pages);
-    return (long long)r * PAGE * max_pages + j;
+  __device__ __forceinline__ long long slot(int r, int j) const { return (long long)r * PAGE * max_pages + j; }
+  // (checked build) whether there is such a row, such a slot: what uses one asks
+  // first and leaves the access out if not
+  __device__ __forceinline__ bool has_row(int page, int h, int j) const {
+    return dbg_ok(page >= 0 && page < num_pages && h >= 0 && h < H && j >= 0);
+  }
+  __device__ __forceinline__ bool has_slot(int r, int j) const {
+    return dbg_ok(r >= 0 && r < B * H && j >= 0 && j < PAGE * max_pages);
   }
 };
 
@@ -91,12 +95,12 @@ append_kernel(Args a, const uint4 *__restrict__ k_new, const uint4 *__restrict__
     }
     const int j = len - c + i;
     const int p = a.page(b, j);
-    if (p >= 0) {
+    if (p >= 0 && a.has_row(p, h, j)) {
       const long long dst = a.row(p, h, j) * CPR + chunk;
       a.k[dst] = k;
       a.v[dst] = v;
     }
-    if (chunk == 0) {
+    if (chunk == 0 && a.has_slot(r, j)) {
       if (a.pos != nullptr) a.pos[a.slot(r, j)] = a.seen[r] - c + i;
       if (a.weight != nullptr) a.weight[a.slot(r, j)] = 0.0f;
     }
@@ -161,9 +165,13 @@ __device__ __forceinline__ void move_pairs(const Args &a, int r, const int *hole
     float w = 0.0f;
     if ((int)threadIdx.x < PAIRS && i0 + (int)threadIdx.x < n) {
       to = holes[i0 + threadIdx.x];
-      const long long of = a.slot(r, fills[i0 + threadIdx.x]);
-      p = a.pos[of];
-      w = a.weight[of];
+      const int from = fills[i0 + threadIdx.x];
+      if (a.has_slot(r, to) && a.has_slot(r, from)) {
+        p = a.pos[a.slot(r, from)];
+        w = a.weight[a.slot(r, from)];
+      } else {
+        to = -1;
+      }
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
@@ -171,8 +179,9 @@ __device__ __forceinline__ void move_pairs(const Args &a, int r, const int *hole
       dst[u] = -1;
       if (i < n) {
         const int into = holes[i], from = fills[i];
+        if (!a.has_slot(r, into) || !a.has_slot(r, from)) continue;
         const int pt = a.page(b, into), pf = a.page(b, from);
-        if (pt >= 0 && pf >= 0) {
+        if (pt >= 0 && pf >= 0 && a.has_row(pt, h, into) && a.has_row(pf, h, from)) {
           const long long src = a.row(pf, h, from) * CPR + chunk;
           dst[u] = a.row(pt, h, into) * CPR + chunk;
           k[u] = a.k[src];
@@ -230,6 +239,7 @@ __device__ __forceinline__ int plan_row(const Args &a, const Evict &ev, int r, i
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (!a.has_slot(r, 0) || !a.has_slot(r, len - 1)) return 0;  // for all CTAs of the row alike
   const int budget = ev.budget, sinks = ev.sinks, cap = ev.cap, from = a.seen[r] - ev.recent;
   const int seg = ((len + ranks - 1) / ranks + 31) / 32 * 32;
   const int begin = min(len, rank * seg), n = min(len, begin + seg) - begin;

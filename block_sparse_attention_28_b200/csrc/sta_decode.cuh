@@ -110,6 +110,11 @@ struct Work {
   int2 *units;        // [units] row, and packed column and filled slots, of a page; else -1
   float *scores;      // [units][M][PAGE] s_j log2 e, -inf out of view
   float *lse2;        // [rows][M] log-sum-exp (log2)
+  // (checked build) parts there is room for, units (0 without weights), rows
+  int part_room, unit_room, row_room;
+  __device__ __forceinline__ bool has_part(int part) const { return dbg_ok(part >= 0 && part < part_room); }
+  __device__ __forceinline__ bool has_unit(int unit) const { return dbg_ok(unit >= 0 && unit < unit_room); }
+  __device__ __forceinline__ bool has_row(int r) const { return dbg_ok(r >= 0 && r < row_room); }
 };
 
 // A page's column (below 2^24) and its filled slots (1 to PAGE).
@@ -140,7 +145,6 @@ struct Num<__nv_bfloat16> {
   static __device__ __forceinline__ float2 unpack(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
   }
-  static __device__ __forceinline__ __nv_bfloat16 round(float x) { return __float2bfloat16_rn(x); }
   static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
@@ -162,7 +166,6 @@ struct Num<__half> {
   static __device__ __forceinline__ float2 unpack(uint32_t v) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&v));
   }
-  static __device__ __forceinline__ __half round(float x) { return __float2half_rn(x); }
   static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
@@ -365,7 +368,8 @@ struct Producer {
       if (col >= 0) {
         // (both on their way at once)
         const int given = a.table[(long long)b * a.max_pages + col];
-        if (s.by_position) newer = newer_halves(a.pos + a.slot(w_row, col * PAGE), a.seen[w_row], s.n_q, len - col * PAGE);
+        if (s.by_position && a.has_slot(w_row, col * PAGE))
+          newer = newer_halves(a.pos + a.slot(w_row, col * PAGE), a.seen[w_row], s.n_q, len - col * PAGE);
         page = a.checked_page(given);
       }
       if (page >= 0) {
@@ -383,9 +387,10 @@ struct Producer {
       if (w_unit == u1 - 1 || (i == n - 1 && w_unit == u1 - 2)) w_flags |= END;
       if (begins) w_flags |= BEGINS;
       if (begins && start + n <= u1) w_flags |= WHOLE;
-      if (i == 0 && work.row_units != nullptr) work.row_units[w_row] = make_int2(start, w_flags & WHOLE ? 0 : n);
+      if (i == 0 && work.row_units != nullptr && work.has_row(w_row))
+        work.row_units[w_row] = make_int2(start, w_flags & WHOLE ? 0 : n);
     }
-    if (work.units != nullptr && lane < take)
+    if (work.units != nullptr && lane < take && work.has_unit(w_unit))
       work.units[w_unit] = col >= 0 ? make_int2(w_row, pack_page(col, w_held)) : make_int2(-1, -1);
     left = __ballot_sync(0xFFFFFFFFu, page_unit);
     // the unit after these, counted from the last one's row
@@ -416,14 +421,15 @@ struct Producer {
       else
         flags &= ~UPPER;
       if (!last) flags &= ~(LAST | END);
+      const int y = w_y + upper * KEYS;
+      if (!(flags & SKIP) && !dbg_ok(y >= 0 && y <= (a.num_pages * a.H - 1) * PAGE + KEYS && (y & (KEYS - 1)) == 0))
+        flags |= SKIP;
       if (issued < stages || wait(&empty[stage], ((issued / stages) & 1) ^ 1, abort, limit)) {
         piece[stage] = Piece{w_row, w_unit, w_held - upper * KEYS, flags};
         if (flags & SKIP) {
           tc::mbar_arrive(&full[stage]);
         } else {
           const uint32_t dst = tc::smem_u32(ring + stage * C::STAGE_BYTES);
-          const int y = w_y + upper * KEYS;
-          dbg_ok(y >= 0 && y <= (a.num_pages * a.H - 1) * PAGE + KEYS && (y & (KEYS - 1)) == 0);
           tc::mbar_expect_tx(&full[stage], C::STAGE_BYTES);
 #pragma unroll
           for (int e = 0; e < D / 64; ++e) tc::tma_load_2d(dst + e * HALF_BYTES, &tk, &full[stage], 64 * e, y);
@@ -798,7 +804,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
       for (int r = lo; r < hi; ++r)
         if (r % gridDim.x == blockIdx.x && row_pages(a, s, r).n == 0) {
           sink.put_nothing(a, s, r);
-          work.row_units[r] = make_int2(0, 0);
+          if (work.has_row(r)) work.row_units[r] = make_int2(0, 0);
         }
     const int upto = cache::warp_scan(mine);
     if (lane == 31) warp_units[warp] = upto;
@@ -876,19 +882,24 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
     if (!(d.flags & SKIP) && tile_rows > 0) {
       const uint32_t at = ring + stage * C::STAGE_BYTES;
       float *sc = nullptr;
-      if (MASS) dbg_ok(d.unit >= 0 && d.unit < units && d.row >= 0 && d.row < rows);
-      if (MASS) sc = work.scores + ((long long)d.unit * M + m0) * PAGE + (d.flags & UPPER ? KEYS : 0);
+      int score_rows = tile_rows;
+      if (MASS) {
+        sc = work.scores + ((long long)d.unit * M + m0) * PAGE + (d.flags & UPPER ? KEYS : 0);
+        if (!work.has_unit(d.unit)) score_rows = 0;
+      }
       if (s.by_position ? d.held < KEYS || (d.flags & NEWER) : d.held - (s.n_q - 1) < KEYS) {
         int newer = s.n_q;  // of slot `lane`
         if (lane < d.held) {
           if (!s.by_position)
             newer = newness(s.n_q, lane, d.held);
           else
-            newer = d.flags & NEWER ? newness(s.n_q, a.pos[a.slot(d.row, d.slot() + lane)], a.seen[d.row]) : 0;
+            newer = d.flags & NEWER && a.has_slot(d.row, d.slot() + lane)
+                        ? newness(s.n_q, a.pos[a.slot(d.row, d.slot() + lane)], a.seen[d.row])
+                        : 0;
         }
-        attend_slots<D, NT, T, MASS, true>(at, lanes, qb, s, token, d.held, newer, acc, sc, tile_rows);
+        attend_slots<D, NT, T, MASS, true>(at, lanes, qb, s, token, d.held, newer, acc, sc, score_rows);
       } else {
-        attend_slots<D, NT, T, MASS, false>(at, lanes, qb, s, token, d.held, 0, acc, sc, tile_rows);
+        attend_slots<D, NT, T, MASS, false>(at, lanes, qb, s, token, d.held, 0, acc, sc, score_rows);
       }
     }
     __syncwarp();
@@ -897,7 +908,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
       stage = 0;
       parity ^= 1;
     }
-    if (!CLUSTER && (d.flags & LAST)) {
+    if (!CLUSTER && (d.flags & LAST) &&
+        (d.flags & WHOLE ? work.has_row(d.row) : work.has_part(cache::part_of(worker, d.flags & BEGINS)))) {
       const long long part = (long long)cache::part_of(worker, d.flags & BEGINS) * M + m0;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -1041,7 +1053,7 @@ join_kernel(const Args a, const Shape s, const Sink<D, T> sink, const Work work,
       for (int x = 0; x < JOIN_BATCH; ++x) {
         const int cx = c + x * (JOIN_THREADS / wide);
         p[x].sum = 0.0f;
-        if (cx <= c1) {
+        if (cx <= c1 && work.has_part(cache::part_of(cx, cx == c0))) {
           const long long at = (long long)cache::part_of(cx, cx == c0) * M + m;
           const float2 ml = work.part_ml[at];
           p[x] = Part{ml.x, ml.y, *reinterpret_cast<const float4 *>(work.part_o + at * D + e % (D / 4) * 4)};
@@ -1082,7 +1094,8 @@ weigh_kernel(const Args a, const int M, const Work work) {
     const int2 next = u < units - step ? work.units[u + step] : make_int2(-1, -1);
     const int col = at.y & 0xFFFFFF;
     // (the bounds hold for whatever a call that was given up has left here)
-    if (at.x >= 0 && at.x < rows && at.y >= 0 && col < a.max_pages && j <= at.y >> 24) {
+    if (at.x >= 0 && at.x < rows && at.y >= 0 && col < a.max_pages && j <= at.y >> 24 && work.has_unit(u) &&
+        a.has_slot(at.x, col * PAGE + j)) {
       const float *x = work.scores + (long long)u * M * PAGE + j, *y = work.lse2 + (long long)at.x * M;
       float *w = a.weight + a.slot(at.x, col * PAGE + j);
       const float old = *w;

@@ -488,10 +488,13 @@ struct DecodeWs {
   size_t part_o, part_ml, row_units, header, units, scores, lse2, total;
 };
 
+// Two parts of every worker.
+int decode_parts(const sta_kv_cache *c, int M) { return 2 * decode::MAX_CTAS * decode::workers_of(c->d, M); }
+
 DecodeWs decode_ws_layout(const sta_kv_cache *c, int group, int n_q, bool accumulate) {
   const size_t M = (size_t)group * n_q, rows = (size_t)c->B * c->kv_heads;
   const size_t units = accumulate ? rows * (c->max_pages + cache::ROW_COST) : 0;
-  const size_t parts = 2 * (size_t)decode::MAX_CTAS * decode::workers_of(c->d, (int)M);
+  const size_t parts = (size_t)decode_parts(c, (int)M);
   DecodeWs w;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -552,6 +555,9 @@ sta_status launch_decode(const sta_kv_cache *c, const cache::Args &a, const deco
   work.units = MASS ? reinterpret_cast<int2 *>(ws + w.units) : nullptr;
   work.scores = MASS ? reinterpret_cast<float *>(ws + w.scores) : nullptr;
   work.lse2 = MASS ? reinterpret_cast<float *>(ws + w.lse2) : nullptr;
+  work.row_room = c->B * c->kv_heads;
+  work.part_room = decode_parts(c, M);
+  work.unit_room = MASS ? work.row_room * (c->max_pages + cache::ROW_COST) : 0;
   decode::Sink<D, T> sink;
   sink.o = static_cast<T *>(o);
   sink.lse = lse;

@@ -450,9 +450,13 @@ sta_status sta_cache_append(const sta_kv_cache *cache, const void *k_new, const 
  * largest weight, whichever is more.
  * q_heads is a multiple of kv_heads, n_q * q_heads / kv_heads <= 64.
  * workspace: device, >= sta_attn_fwd_cached_workspace() bytes (0 for sizes the
- * call rejects; with accumulate 256 bytes for every page, head and query row),
- * 256-aligned; nothing in it has to start at zero, and calls
- * that overlap on the GPU need one each. Deterministic. */
+ * call rejects), 256-aligned; nothing in it has to start at zero, and calls
+ * that overlap on the GPU need one each. With accumulate it holds every score:
+ * 256 bytes for every head, query row and column of page_table, filled or not
+ * (how many are, only the device knows). Deterministic: the same call gives the
+ * same bits. Rows are summed up in parts that go by B, the heads, max_pages, the
+ * lengths and accumulate, so calls that differ in one of these may differ in
+ * the last bits of o and lse. */
 size_t sta_attn_fwd_cached_workspace(const sta_kv_cache *cache, int32_t q_heads, int32_t n_q, int32_t accumulate);
 sta_status sta_attn_fwd_cached(const sta_kv_cache *cache, const void *q, void *o, float *lse, int32_t q_heads,
                                int32_t n_q, const int32_t *page_ptr, const int32_t *page_idx,

@@ -10,10 +10,12 @@
 // query; only in those (and where a row ends) the warps mask scores.
 //
 // Every key and value is read once and used by the M <= 64 query rows of its
-// head: at most 64 flop per byte, so HBM bounds the call. The matrix products
-// are mma.sync tiles with the keys (or the values' columns) along the 16 rows
-// and 8 query rows across: S^T = K Q^T, O^T = V^T P^T. (A tcgen05 tile has 64
-// rows at least; a token of a group of 1 to 8 heads has 8 to offer.)
+// head: at most 64 flop per byte, so HBM is the floor. The matrix products are
+// mma.sync tiles with the keys (or the values' columns) along the 16 rows and 8
+// query rows across: S^T = K Q^T, O^T = V^T P^T. Up to 16 query rows that keeps
+// up with HBM (tensor pipe 15% busy). With 17 to 64 the warps wait for their own
+// products instead (a quarter to a third of HBM's rate); tcgen05 tiles, 128
+// keys by the query rows, would fit there and have not been built.
 //
 // attend_kernel: one CTA per SM, 7 or 8 warps. A worker is a warp (for many
 // query rows two or four, see rows_per_warp) with a ring of its own in shared

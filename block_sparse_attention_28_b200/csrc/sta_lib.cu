@@ -520,7 +520,9 @@ DecodeWs decode_ws_layout(const sta_kv_cache *c, int group, int n_q, bool accumu
 // joining of the larger parts costs more than it saves. 1 x 2 heads of 1,024
 // tokens: 7.6 us (general form: 9.2); 16 x 8 heads of 850: 15.5 (18.3), but
 // 8 heads of 4,000, two pages to a worker instead of one: 12.8 (10.8), and 16
-// query rows of 4 heads of 1,000: 15.2 (13.9).
+// query rows of 4 heads of 1,000: 15.2 (13.9). The lengths are on the device, so
+// this goes by what the page table can hold: short rows under a wide table take
+// the general form.
 int row_cluster(const sta_kv_cache *c, int M) {
   const long long rows = (long long)c->B * c->kv_heads;
   if (M > 8 || rows > decode::MAX_CTAS) return 0;

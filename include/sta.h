@@ -475,6 +475,9 @@ sta_status sta_attn_fwd_cached(const sta_kv_cache *cache, const void *q, void *o
  * Slots are therefore not in order of position afterwards, the newest tokens
  * among them; attention goes by position. Tokens appended since the last
  * attention over them have no weight yet: recent >= their number keeps them.
+ * Tokens that are to be taken back (drafts that were not accepted: lens and
+ * seen lowered by their number) have to be the last slots still, so that is
+ * done before an eviction.
  * Needs seen, slot_pos and weight. budget >= 1, recent >= 0, sinks >= 0,
  * recent + sinks <= budget. workspace: device, >= sta_cache_evict_workspace()
  * bytes, 256-aligned; nothing in it has to start at zero, and calls that

@@ -7,7 +7,7 @@ import torch
 
 import _cache as C
 from oracle import kv_cache as K
-from test_gpu_cache import attend, cache_of, evict, ok, shuffled, sta  # noqa: F401
+from test_gpu_cache import attend, cache_of, evict, garbage, ok, shuffled, sta  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +130,86 @@ def test_drafts_after_evictions(sta, d, dtype, kv, group, n_q, budget, accumulat
     # at some step the newest tokens were not the last slots in order (with equal weights they are: the first slots
     # stay, and the newest tokens fill the last ones)
     assert moved or not accumulate
+
+
+def test_drafts_that_the_eviction_gave_up(sta):  # noqa: F811
+    """Nothing recent is protected and the drafts have no weight: some are gone
+    when they are attended for, the others are seen by position as ever."""
+    n_q, kv, d = 5, 2, 64
+    t = C.make([120, 75], kv, d, "bf16", seed=41, room=n_q)
+    new = [C.queries(2, n_q, kv, d, "bf16", seed=s) for s in (1, 2)]
+    t["lens"] += n_q
+    t["seen"] += n_q
+    sta.sta_cache_append(cache_of(sta, t), *new)
+    t["weight"][0, :, 121] = 1e9  # one draft that is heavy all the same
+    t["weight"][0, :, 123] = 1e9
+    evict(sta, t, 78, 0, 0)
+    ok(sta)
+    newest = (t["slot_pos"][0, :, :78] >= 120).sum(-1)
+    assert (newest == 2).all() and t["lens"].tolist() == [[78, 78], [78, 78]]
+    compare(sta, t, C.queries(2, n_q, kv * 2, d, "bf16", seed=4), "bf16", accumulate=True)
+
+
+def test_drafts_taken_back_before_the_eviction(sta):  # noqa: F811
+    """Append four drafts, attend, take two back, evict, and go on: what was
+    taken back is overwritten, the rest goes by position."""
+    n_q, kv, d, budget = 4, 2, 128, 90
+    t = C.make([88, 200], kv, d, "fp16", seed=42, room=80)
+    c = C.oracle(t)
+    for k in range(6):
+        new = [C.queries(2, n_q, kv, d, "fp16", seed=10 * k + s) for s in (1, 2)]
+        for x in ("lens", "seen"):
+            t[x] += n_q
+            c[x] += n_q
+        sta.sta_cache_append(cache_of(sta, t), *new)
+        K.append(c, *(x.double().cpu().numpy() for x in new))
+        compare(sta, t, C.queries(2, n_q, kv * 4, d, "fp16", seed=k), "fp16", accumulate=True)
+        for x in ("lens", "seen"):
+            t[x] -= 2
+            c[x] -= 2
+        c["weight"] = t["weight"].double().cpu().numpy()
+        evict(sta, t, budget, 8, 2)
+        ok(sta)
+        K.evict(c, budget, 8, 2)
+        C.same_as(t, c)
+
+
+def test_captured_steps_with_drafts(sta):  # noqa: F811
+    """Append three tokens, evict, attend and accumulate, captured once and
+    replayed, against the same calls made one by one on another stream."""
+    n_q, kv, group, d, budget = 3, 2, 4, 64, 70
+    t = C.make([60, 100], kv, d, "bf16", seed=43, room=40)
+    ref = {n: x.clone() for n, x in t.items()}
+    k_new, v_new = (C.queries(2, n_q, kv, d, "bf16", seed=s) for s in (1, 2))
+    q = C.queries(2, n_q, kv * group, d, "bf16", seed=3)
+
+    def buffers(t):
+        cache = cache_of(sta, t)
+        return (cache, torch.empty_like(q), torch.empty(2, kv * group, n_q, device="cuda"),
+                garbage(sta.sta_attn_fwd_cached_workspace(cache, kv * group, n_q, True)),
+                garbage(sta.sta_cache_evict_workspace(cache, budget)))
+
+    def step(t, cache, o, lse, ws, ews):
+        t["lens"].add_(n_q)
+        t["seen"].add_(n_q)
+        sta.sta_cache_append(cache, k_new, v_new)
+        sta.sta_cache_evict(cache, budget, n_q, 1, ews)
+        sta.sta_attn_fwd_cached(cache, q, o, lse, ws, accumulate=True)
+
+    mine, theirs, side = buffers(t), buffers(ref), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(t, *mine)
+    for _ in range(8):
+        k_new.normal_()
+        q.normal_()
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(side):
+            step(ref, *theirs)
+        torch.cuda.synchronize()
+        assert torch.equal(C.bits(mine[1]), C.bits(theirs[1])) and torch.equal(mine[2], theirs[2])
+    ok(sta)
+    for n in ("lens", "seen", "slot_pos", "weight"):
+        assert torch.equal(t[n], ref[n])

@@ -152,20 +152,20 @@ struct alignas(16) Tally {
 // destinations are disjoint.
 template <int D, int THREADS, int UNROLL>
 __device__ __forceinline__ void move_pairs(const Args &a, int r, const int *holes, const int *fills, int n, int i0,
-                                           int step) {
+                                           int step, int tid) {
   constexpr int CPR = D / 8;
   constexpr int GROUPS = THREADS / CPR, PAIRS = GROUPS * UNROLL;
   static_assert(PAIRS <= THREADS, "a thread for every pair");
   const int b = r / a.H, h = r - b * a.H;
-  const int chunk = threadIdx.x % CPR, group = threadIdx.x / CPR;
+  const int chunk = tid % CPR, group = tid / CPR;
   for (; i0 < n; i0 += step) {
     uint4 k[UNROLL], v[UNROLL];
     long long dst[UNROLL];
     int to = -1, p = 0;
     float w = 0.0f;
-    if ((int)threadIdx.x < PAIRS && i0 + (int)threadIdx.x < n) {
-      to = holes[i0 + threadIdx.x];
-      const int from = fills[i0 + threadIdx.x];
+    if (tid < PAIRS && i0 + tid < n) {
+      to = holes[i0 + tid];
+      const int from = fills[i0 + tid];
       if (a.has_slot(r, to) && a.has_slot(r, from)) {
         p = a.pos[a.slot(r, from)];
         w = a.weight[a.slot(r, from)];
@@ -210,8 +210,18 @@ struct Evict {
   int *count;           // [rows] pairs that are left to move_kernel
 };
 
-// Plans row r, which has len > budget slots: a CTA, or (CLUSTER) those of a
-// cluster, each with an equal range of the slots and their keys in shared
+// What plans a row: half a CTA of 1024 threads, a CTA, the CTAs of a cluster.
+enum : int { BY_HALF, BY_CTA, BY_CLUSTER };
+template <int BY>
+__device__ __forceinline__ void sync_threads() {  // of a half, or of the CTA
+  if (BY == BY_HALF)
+    asm volatile("barrier.sync %0, 512;" ::"r"(1 + (int)(threadIdx.x >> 9)) : "memory");
+  else
+    __syncthreads();
+}
+
+// Plans row r, which has len > budget slots: THREADS threads of a CTA, or those
+// of a cluster's CTAs, each with an equal range of the slots and their keys in shared
 // memory (read once; past key_room they are read again). The budget-th largest
 // key is found by radix selection on histograms that every CTA sums up over the
 // cluster; one more pass over the keys counts ties, holes (slots given up below
@@ -221,24 +231,31 @@ struct Evict {
 // (0 to the others). The key reads (8 bytes per slot) are the floor; what bounds
 // it is latency: some ten steps that each wait for the one before (and, at
 // 25,000 keys to a CTA, the instructions of the five passes over them).
-template <int THREADS, bool CLUSTER>
+template <int THREADS, int BY>
 __device__ __forceinline__ int plan_row(const Args &a, const Evict &ev, int r, int len, unsigned *plan_smem,
                                         int key_room) {
   constexpr int W = THREADS / 32;
   constexpr int PER = PLAN_BINS / THREADS;  // bins of a thread
+  constexpr bool CLUSTER = BY == BY_CLUSTER;
   constexpr int MOST = CLUSTER ? PLAN_RANKS : 1;
   constexpr bool ROOM = THREADS == 512;  // for all keys
   constexpr int KEYS = THREADS == 1024 ? 4 : 2;  // keys of a thread read from shared memory at once: what registers hold
   unsigned *hist = plan_smem;                            // [PLAN_PASSES][PLAN_BINS]
   unsigned *keys = plan_smem + PLAN_PASSES * PLAN_BINS;  // [key_room]
-  __shared__ int part[W];
-  __shared__ Tally tally[W], whole;
-  __shared__ unsigned s_bin;
-  __shared__ int s_left;
+  constexpr int HALVES = BY == BY_HALF ? 2 : 1;
+  __shared__ int parts[HALVES][W];
+  __shared__ Tally tallies[HALVES][W], whole;
+  __shared__ unsigned bins[HALVES];
+  __shared__ int lefts[HALVES];
+  const int half = BY == BY_HALF ? threadIdx.x >> 9 : 0;
+  int *part = parts[half];
+  Tally *tally = tallies[half];
+  unsigned &s_bin = bins[half];
+  int &s_left = lefts[half];
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x & (THREADS - 1), lane = tid & 31, warp = tid >> 5;
   if (!a.has_slot(r, 0) || !a.has_slot(r, len - 1)) return 0;  // for all CTAs of the row alike
   const int budget = ev.budget, sinks = ev.sinks, cap = ev.cap, from = a.seen[r] - ev.recent;
   const int seg = ((len + ranks - 1) / ranks + 31) / 32 * 32;
@@ -263,7 +280,7 @@ __device__ __forceinline__ int plan_row(const Args &a, const Evict &ev, int r, i
   };
 
   for (int i = tid; i < PLAN_PASSES * PLAN_BINS; i += THREADS) hist[i] = 0;
-  __syncthreads();
+  sync_threads<BY>();
   for (int j0 = tid; j0 < n; j0 += THREADS * PLAN_UNROLL) {
     float w[PLAN_UNROLL];
     int p[PLAN_UNROLL];
@@ -304,7 +321,7 @@ __device__ __forceinline__ int plan_row(const Args &a, const Evict &ev, int r, i
     if (CLUSTER)
       cluster.sync();
     else
-      __syncthreads();
+      sync_threads<BY>();
     // the bin, counted from the top, in which the left-th key lies; this
     // thread's bins are PLAN_BINS - 1 - PER tid and the PER - 1 below
     int sum[PER], all = 0;
@@ -321,7 +338,7 @@ __device__ __forceinline__ int plan_row(const Args &a, const Evict &ev, int r, i
     for (int x = 0; x < PER; ++x) all += sum[x];
     const int upto = warp_scan(all);
     if (lane == 31) part[warp] = upto;
-    __syncthreads();
+    sync_threads<BY>();
     int before = upto - all + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? part[lane] : 0);
     if (before < left && left <= before + all) {
       int x = 0;
@@ -334,7 +351,7 @@ __device__ __forceinline__ int plan_row(const Args &a, const Evict &ev, int r, i
       s_bin = (unsigned)(PLAN_BINS - 1 - PER * tid - x);
       s_left = left - before;
     }
-    __syncthreads();
+    sync_threads<BY>();
     threshold = (threshold << bits) | s_bin;
     left = s_left;
   }
@@ -364,7 +381,7 @@ __device__ __forceinline__ int plan_row(const Args &a, const Evict &ev, int r, i
   mine.hole = __reduce_add_sync(0xFFFFFFFFu, mine.hole);
   mine.fill = hi - mid - mine.tie_above - __reduce_add_sync(0xFFFFFFFFu, given_up);
   if (lane == 0) tally[warp] = mine;
-  __syncthreads();
+  sync_threads<BY>();
   if (warp == 0) {
     Tally v = {0, 0, 0, 0};
     if (lane < W) v = tally[lane];
@@ -377,7 +394,7 @@ __device__ __forceinline__ int plan_row(const Args &a, const Evict &ev, int r, i
   if (CLUSTER)
     cluster.sync();
   else
-    __syncthreads();
+    sync_threads<BY>();
   // ties, holes and fills before this warp's range
   int tie = 0, hole = 0, fill = 0;
   auto pass_over = [&](const Tally &v) {  // a lane's each, in the order of the lanes
@@ -441,101 +458,113 @@ __device__ __forceinline__ int plan_row(const Args &a, const Evict &ev, int r, i
   if (CLUSTER)
     cluster.sync();
   else
-    __syncthreads();
+    sync_threads<BY>();
   return pairs;
 }
 
-// Which kernel plans a row goes by the slots it holds, not by the width of the
-// page table, which a caller makes for the longest context it admits: up to
-// PLAN_SHORT slots 512 threads, three rows to an SM; more than those, 1024
-// threads or a cluster.
+// How a row is planned goes by the slots it holds, not by the width of the page
+// table, which a caller makes for the longest context it admits: up to
+// PLAN_SHORT slots 512 threads (where there are rows enough for that), more than
+// those a CTA of 1024, or a cluster.
 constexpr int PLAN_SHORT = 4096;
 
-// A CTA per row of at most PLAN_SHORT slots, which also moves its pairs where
-// there are PLAN_MOVES at most, as in a cache that is cut at every step.
+// 512 threads that plan a row also move its pairs where there are PLAN_MOVES at
+// most, as in a cache that is cut at every step.
 constexpr int PLAN_MOVES = PAGE;
+template <int D, int BY>
+__device__ __forceinline__ void plan_short_row(const Args &a, const Evict &ev, int r, int len, unsigned *plan_smem,
+                                               int key_room) {
+  constexpr int HALVES = BY == BY_HALF ? 2 : 1;
+  __shared__ int pairs[HALVES];
+  const int half = BY == BY_HALF ? threadIdx.x >> 9 : 0, tid = threadIdx.x & 511;
+  const int got = plan_row<512, BY>(a, ev, r, len, plan_smem, key_room);
+  if (tid == 512 - 32) {
+    pairs[half] = got;
+    ev.count[r] = got <= PLAN_MOVES ? 0 : got;
+  }
+  sync_threads<BY>();
+  if (pairs[half] <= PLAN_MOVES)
+    move_pairs<D, 512, 2>(a, r, ev.holes + (long long)r * ev.cap, ev.fills + (long long)r * ev.cap, pairs[half], 0,
+                          512 / (D / 8) * 2, tid);
+}
+
+// Under a table of up to PLAN_SHORT slots: a CTA per row.
 template <int D>
 __global__ void __launch_bounds__(512, 3)
 evict_short_kernel(const Args a, const Evict ev, int key_room) {
   extern __shared__ unsigned plan_smem[];
-  __shared__ int s_pairs;
-  const int r = blockIdx.x, tid = threadIdx.x;
+  const int r = blockIdx.x;
   let_next_start();
   wait_for_previous();
   const int len = a.length(r);
-  if (len <= ev.budget || len > PLAN_SHORT) {
-    if (tid == 0) ev.count[r] = 0;
+  if (len <= ev.budget) {
+    if (threadIdx.x == 0) ev.count[r] = 0;
     return;
   }
-  const int got = plan_row<512, false>(a, ev, r, len, plan_smem, key_room);
-  if (tid == 512 - 32) {
-    s_pairs = got;
-    ev.count[r] = got <= PLAN_MOVES ? 0 : got;
-  }
-  __syncthreads();
-  if (s_pairs <= PLAN_MOVES)
-    move_pairs<D, 512, 2>(a, r, ev.holes + (long long)r * ev.cap, ev.fills + (long long)r * ev.cap, s_pairs, 0,
-                          512 / (D / 8) * 2);
+  plan_short_row<D, BY_CTA>(a, ev, r, len, plan_smem, key_room);
 }
 
-// Rows of more than `above` slots (the others are evict_short_kernel's; -1:
-// there is none, and count is written for all rows). Those of up to `alone`
-// slots have a CTA each, the others a cluster; both stride over the rows. The
-// first warp looks for them, 32 lengths at a time, and leaves what it finds in
-// shared memory (held in registers it made the plan spill: 134 us at 40 rows of
-// 75,600 slots became 144). All CTAs of a cluster find the same rows: a row is
-// one cluster's alone, and its length changes only at the end of its plan.
+// Under a wider one, as many CTAs as run at once. A row is one cluster's, which
+// looks its rows up 32 at a time and plans those of more than `alone` slots with
+// all of its CTAs, then those of more than `halved` a CTA each, then the others
+// half a CTA each. What a warp finds is left in shared memory (held in registers
+// it made the plan spill: 134 us at 40 rows of 75,600 slots became 144).
+template <int D>
 __global__ void __launch_bounds__(1024, 1)
-evict_long_kernel(const Args a, const Evict ev, int above, int alone, int key_room) {
+evict_long_kernel(const Args a, const Evict ev, int halved, int alone, int key_room) {
   extern __shared__ unsigned plan_smem[];
-  __shared__ int s_row[32], s_len[32], s_found;
-  __shared__ long long s_next;
+  __shared__ int s_row[3][32], s_len[3][32], s_found[3];
+  __shared__ long long s_first;
   namespace cg = cooperative_groups;
   let_next_start();
   wait_for_previous();
-  auto plan_rows = [&](auto with_cluster) {
-    constexpr bool TOGETHER = decltype(with_cluster)::value;
-    if (threadIdx.x == 0) {
-      const int ranks = (int)cg::this_cluster().num_blocks(), clusters = (int)gridDim.x / ranks;
-      s_next = (int)blockIdx.x / ranks + (TOGETHER ? 0 : (int)cg::this_cluster().block_rank() * clusters);
-    }
-    while (true) {
-      __syncthreads();
-      if (threadIdx.x < 32) {
-        const int lane = threadIdx.x, rows = a.B * a.H;
-        const int step = TOGETHER ? (int)gridDim.x / (int)cg::this_cluster().num_blocks() : (int)gridDim.x;
-        long long r0 = s_next;
-        unsigned todo = 0;
-        for (; todo == 0 && r0 < rows; r0 += 32LL * step) {
-          const long long mine = r0 + (long long)lane * step;
-          const int len = mine < rows ? (TOGETHER ? a.lens[mine] : a.length((int)mine)) : -1;
-          const bool cut = length_ok(len, a.max_pages) && len > ev.budget && len > above;
-          if (!TOGETHER && above < 0 && !cut && mine < rows) ev.count[mine] = 0;
-          todo = __ballot_sync(0xFFFFFFFFu, cut && (len > alone) == TOGETHER);
-          if (todo >> lane & 1) {
-            const int at = __popc(todo & ((1u << lane) - 1u));
-            s_row[at] = (int)mine;
-            s_len[at] = len;
-          }
+  if (threadIdx.x == 0) s_first = blockIdx.x / cg::this_cluster().num_blocks();
+  while (true) {
+    __syncthreads();
+    const long long first = s_first;
+    if (first >= a.B * a.H) break;
+    if (threadIdx.x < 32) {
+      const int lane = threadIdx.x, ranks = (int)cg::this_cluster().num_blocks(), clusters = (int)gridDim.x / ranks;
+      const long long mine = first + (long long)lane * clusters;
+      const int len = mine < a.B * a.H ? a.length((int)mine) : -1;
+      const bool cut = len > ev.budget;
+      if (mine < a.B * a.H && !cut && cg::this_cluster().block_rank() == 0) ev.count[mine] = 0;
+      const int kind = len <= halved ? BY_HALF : (len <= alone ? BY_CTA : BY_CLUSTER);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const unsigned some = __ballot_sync(0xFFFFFFFFu, cut && kind == k);
+        const int at = __popc(some & ((1u << lane) - 1u));
+        if (cut && kind == k) {
+          s_row[k][at] = (int)mine;
+          s_len[k][at] = len;
         }
-        __syncwarp();
-        if (lane == 0) {
-          s_found = __popc(todo);
-          s_next = r0;
-        }
-      }
-      __syncthreads();
-      if (s_found == 0) break;
-      for (int i = 0; i < s_found; ++i) {
-        const int got = plan_row<1024, TOGETHER>(a, ev, s_row[i], s_len[i], plan_smem, key_room);
-        if (threadIdx.x == 1024 - 32 &&
-            (!TOGETHER || cg::this_cluster().block_rank() + 1 == cg::this_cluster().num_blocks()))
-          ev.count[s_row[i]] = got;
+        if (lane == 0) s_found[k] = __popc(some);
       }
     }
-  };
-  plan_rows(std::false_type{});
-  if (cg::this_cluster().num_blocks() > 1) plan_rows(std::true_type{});
+    // all CTAs have read the lengths before any plan changes one
+    if (cg::this_cluster().num_blocks() > 1)
+      cg::this_cluster().sync();
+    else
+      __syncthreads();
+    // (everyone has read it, and reads it again behind the next barrier)
+    if (threadIdx.x == 0) s_first = first + 32LL * (gridDim.x / cg::this_cluster().num_blocks());
+    if (cg::this_cluster().num_blocks() > 1)
+      for (int i = 0; i < s_found[BY_CLUSTER]; ++i) {
+        const int got =
+            plan_row<1024, BY_CLUSTER>(a, ev, s_row[BY_CLUSTER][i], s_len[BY_CLUSTER][i], plan_smem, key_room);
+        if (threadIdx.x == 1024 - 32 && cg::this_cluster().block_rank() + 1 == cg::this_cluster().num_blocks())
+          ev.count[s_row[BY_CLUSTER][i]] = got;
+      }
+    for (int i = (int)cg::this_cluster().block_rank(); i < s_found[BY_CTA];
+         i += (int)cg::this_cluster().num_blocks()) {
+      const int got = plan_row<1024, BY_CTA>(a, ev, s_row[BY_CTA][i], s_len[BY_CTA][i], plan_smem, key_room);
+      if (threadIdx.x == 1024 - 32) ev.count[s_row[BY_CTA][i]] = got;
+    }
+    for (int i = 2 * (int)cg::this_cluster().block_rank() + (int)(threadIdx.x >> 9); i < s_found[BY_HALF];
+         i += 2 * (int)cg::this_cluster().num_blocks())
+      plan_short_row<D, BY_HALF>(a, ev, s_row[BY_HALF][i], s_len[BY_HALF][i],
+                                 plan_smem + (threadIdx.x >> 9) * (PLAN_PASSES * PLAN_BINS + PLAN_SHORT), PLAN_SHORT);
+  }
 }
 
 constexpr int MOVE_THREADS = 128;
@@ -554,7 +583,8 @@ move_kernel(const Args a, int cap, const int *holes, const int *fills, const int
   wait_for_previous();
   const int r = blockIdx.x;
   move_pairs<D, MOVE_THREADS, MOVE_UNROLL>(a, r, holes + (long long)r * cap, fills + (long long)r * cap, count[r],
-                                           (int)blockIdx.y * move_share<D>(), (int)gridDim.y * move_share<D>());
+                                           (int)blockIdx.y * move_share<D>(), (int)gridDim.y * move_share<D>(),
+                                           (int)threadIdx.x);
 }
 
 }  // namespace cache

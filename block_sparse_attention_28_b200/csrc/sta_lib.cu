@@ -670,8 +670,11 @@ long long clusters_at_once(int ranks) { return ranks <= 3 ? decode::MAX_CTAS / r
 // memory. The size of the clusters goes by what the page table can hold,
 // whether a row takes one by what it holds: 8 rows of 20,000 slots take 21 us
 // under a table that just holds them (2 CTAs each) and 23 under one of 131,072.
-sta_status launch_long_plan(const sta_kv_cache *c, const cache::Args &a, const cache::Evict &ev, int above,
-                            cudaStream_t s) {
+// Short rows take half a CTA each where there are more rows than SMs (512 rows
+// cut from 1,088 slots to 1,024: 22 us, with a CTA each 26; 8 rows of 4,000: 13
+// and 11).
+template <int D>
+sta_status launch_long_plan(const sta_kv_cache *c, const cache::Args &a, const cache::Evict &ev, cudaStream_t s) {
   const long long rows = (long long)c->B * c->kv_heads, slots = (long long)cache::PAGE * c->max_pages;
   int fit = 4;
   while (fit > 1 && rows > clusters_at_once(fit)) --fit;
@@ -681,20 +684,24 @@ sta_status launch_long_plan(const sta_kv_cache *c, const cache::Args &a, const c
   const int ranks = (int)(most < 1 ? 1 : (most > cache::PLAN_RANKS ? cache::PLAN_RANKS : most));
   // keys of a cluster's CTA, or of a row that has one for itself
   long long share = (slots / ranks + 63) / 32 * 32;
-  share = fit > 1 && share < 2 * 8192 ? 2 * 8192 : share;
+  share = share < 2 * 8192 ? 2 * 8192 : share;
   const int room = (int)(share < cache::PLAN_MAX_KEYS ? share : cache::PLAN_MAX_KEYS);
   const int alone = fit > 1 ? 2 * 8192 - 1 : room;
   const long long clusters = rows < clusters_at_once(ranks) ? rows : clusters_at_once(ranks);
-  const sta_status st = allow_smem(cache::evict_long_kernel, plan_smem(cache::PLAN_MAX_KEYS));
+  // (at least 2 * 8192 keys: two halves have 2 * 4096 and a second histogram)
+  auto kernel = cache::evict_long_kernel<D>;
+  const sta_status st = allow_smem(kernel, plan_smem(cache::PLAN_MAX_KEYS));
   if (st != STA_OK) return st;
-  return launch_early(cache::evict_long_kernel, dim3((unsigned)(clusters * ranks)), 1024, plan_smem(room), ranks, s, a,
-                      ev, above, ranks == 1 ? cache::PAGE * c->max_pages : alone, room);
+  return launch_early(kernel, dim3((unsigned)(clusters * ranks)), 1024, plan_smem(room), ranks, s, a, ev,
+                      rows > decode::MAX_CTAS ? cache::PLAN_SHORT : 0, ranks == 1 ? cache::PAGE * c->max_pages : alone,
+                      room);
 }
 
 // How many pairs a row has only the device knows, and a CTA that finds none
 // costs a nanosecond: 64 CTAs per SM where each SM has a row at most, else 32
-// (168 rows of 1 to 14,911 slots: 64 per SM 30 us, 32 28, 16 30; 512 rows that
-// have moved their pairs already: 26, 21, 18; 40 rows of 75,600: 136, 138, 143).
+// (168 rows of 1 to 14,911 slots: 64 per SM 25 us, 32 22.4, 16 25; 512 rows whose
+// plans have moved the pairs already: 27, 22, 20; 512 rows cut from 4,000 to
+// 2,000: 113, 115, 117; 40 rows of 75,600: 137, 32 per SM 138).
 template <int D>
 sta_status launch_move(const sta_kv_cache *c, const cache::Args &a, const cache::Evict &ev, cudaStream_t s) {
   const long long passes = ((long long)ev.cap + cache::move_share<D>() - 1) / cache::move_share<D>();
@@ -1062,20 +1069,14 @@ sta_status sta_cache_evict(const sta_kv_cache *cache, int32_t budget, int32_t re
   ev.holes = reinterpret_cast<int *>(ws + w.holes);
   ev.fills = reinterpret_cast<int *>(ws + w.fills);
   ev.count = reinterpret_cast<int *>(ws + w.count);
-  // Rows of up to PLAN_SHORT slots have a kernel of their own where there are
-  // more rows than SMs (512 rows cut from 1,088 slots to 1,024 under a table of
-  // 4,160: 21 us, with evict_long_kernel alone 41) or no others.
   const bool wide = cache::PAGE * cache->max_pages > cache::PLAN_SHORT;
-  const bool some_short =
-      !wide || (budget < cache::PLAN_SHORT && (long long)cache->B * cache->kv_heads > decode::MAX_CTAS);
-  sta_status run = STA_OK;
-  if (some_short)
-    run = cache->d == 128 ? launch_short_plan<128>(cache, a, ev, s) : launch_short_plan<64>(cache, a, ev, s);
-  if (run == STA_OK && wide) run = launch_long_plan(cache, a, ev, some_short ? cache::PLAN_SHORT : -1, s);
+  const bool large = cache->d == 128;
+  const sta_status run = wide ? (large ? launch_long_plan<128>(cache, a, ev, s) : launch_long_plan<64>(cache, a, ev, s))
+                              : (large ? launch_short_plan<128>(cache, a, ev, s)
+                                       : launch_short_plan<64>(cache, a, ev, s));
   // (no row has more pairs than the lists hold)
   if (run != STA_OK || w.cap == 0 || (!wide && w.cap <= cache::PLAN_MOVES)) return run;
-  return cache->d == 128 ? launch_move<128>(cache, a, ev, s)
-                         : launch_move<64>(cache, a, ev, s);
+  return large ? launch_move<128>(cache, a, ev, s) : launch_move<64>(cache, a, ev, s);
 }
 
 sta_status sta_set_wait_limit(int64_t limit_cycles) {

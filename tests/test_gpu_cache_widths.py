@@ -69,9 +69,9 @@ LENGTHS = [0, 1, 500, 501, 564, 4096, 4097, 5000, 16_383, 16_384, 20_000, 33_000
 
 @pytest.mark.parametrize("width", [0, 1100, 6400])
 @pytest.mark.parametrize("kv,budget,recent,sinks", [
-    (1, 500, 40, 3),      # few rows: one kernel plans all of them
+    (1, 500, 40, 3),      # few rows: a CTA or a cluster each
     (1, 4096, 700, 9),    # no row of up to 4,096 slots is cut
-    (15, 500, 40, 3),     # more rows than SMs: two kernels
+    (15, 500, 40, 3),     # more rows than SMs: half a CTA each for short ones
     (15, 4500, 40, 3),
     (15, 16_383, 0, 0),
 ])
